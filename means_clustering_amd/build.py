@@ -1,7 +1,7 @@
-"""Build the HIP library ``libkmeans_amd.so`` in-tree for gfx950 (MI355X).
+"""Build the HIP libraries ``libkmeans_amd.so`` and ``libkm_cache.so`` in-tree for gfx950 (MI355X).
 
 Each source is compiled by hipcc to an object under ``_build/`` (in
-parallel), then linked into a shared library next to this file.  Every build
+parallel), then linked into shared libraries next to this file.  Every build
 compiles from scratch, so a stale library is never mistaken for a fresh one.
 """
 from __future__ import annotations
@@ -17,6 +17,10 @@ LIB_NAME = "libkmeans_amd.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["csrc/flash_assign.hip", "csrc/sort.hip", "csrc/reduce.hip", "csrc/small_k.hip", "csrc/api.cpp",
            "csrc/noalloc.hip"]
+# the paged key/value cache (a library of its own)
+CACHE_LIB_PATH = os.path.join(HERE, "libkm_cache.so")
+CACHE_SOURCES = ["csrc/kv_tables.hip", "csrc/kv_append.hip", "csrc/kv_decode.hip", "csrc/kv_chunk.hip",
+                 "csrc/kv_api.cpp"]
 # peak probes for the benchmark's roofline denominators, and the ablation
 # baselines (libraries of their own, not part of libkmeans_amd.so)
 EXTRA_LIBS = [("csrc/peaks.hip", os.path.join(HERE, "libkm_peaks.so"), []),
@@ -51,24 +55,25 @@ def build(verbose: bool = False, jobs: int = 4) -> str:
             print(" ".join(cmd))
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        futs = [ex.submit(compile_one, src) for src in SOURCES]
-        extra = [ex.submit(compile_one, src, flags) for src, _, flags in EXTRA_LIBS]
-        objs = [f.result() for f in futs]
-        extra_objs = [f.result() for f in extra]
-    for (_, path, _), obj in zip(EXTRA_LIBS, extra_objs):
+    def link(path, objs):
         tmp = path + ".tmp"
-        r = subprocess.run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, obj],
+        r = subprocess.run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs],
                            capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr}")
         os.replace(tmp, path)
-    tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
+
+    with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        futs = [ex.submit(compile_one, src) for src in SOURCES]
+        cache = [ex.submit(compile_one, src) for src in CACHE_SOURCES]
+        extra = [ex.submit(compile_one, src, flags) for src, _, flags in EXTRA_LIBS]
+        objs = [f.result() for f in futs]
+        cache_objs = [f.result() for f in cache]
+        extra_objs = [f.result() for f in extra]
+    for (_, path, _), obj in zip(EXTRA_LIBS, extra_objs):
+        link(path, [obj])
+    link(CACHE_LIB_PATH, cache_objs)
+    link(LIB_PATH, objs)
     return LIB_PATH
 
 

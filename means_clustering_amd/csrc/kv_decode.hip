@@ -1,0 +1,416 @@
+// Attention of few rows (at most 16 or 32 for each request and cache head)
+// over a paged cache: the decode step, and the join of divided rows.
+//
+//   s = scale * (K q) + weight,  m = running maximum, p = e^(s - m),
+//   l = sum p,  o = sum p v,  out = o / l
+//
+// The cache is read once and that is what bounds it.  A wavefront takes 32
+// keys at a time, its keys and values straight from memory into registers
+// (one step ahead of the products), and keeps its own m, l and o; the four
+// wavefronts of a workgroup take turns in the keys and are joined at the end.
+//
+// v_mfma_f32_16x16x32 with lane l = 16 g + x: the A operand's lane holds row
+// x, depth 8 g .. 8 g + 7; B's holds column x, the same depths; the result's
+// holds column x, rows 4 g .. 4 g + 3.  The first product is S' = K Q' (rows
+// are keys, columns the query rows), the second O' = V' P', so a lane's
+// maxima, sums and factors belong to one query row.  P' needs no exchange:
+// the lane's results of two 16-key halves are the 8 depths of its group once
+// depth 8 g + j stands for key 4 g + j of half 0 (j < 4) or key 4 g + j - 4
+// of half 1.  V' has to follow that order: the lane loads DV neighbouring
+// columns of those 8 keys, and a byte permute of two keys' words makes the
+// operands of columns DV x + e.
+#include "kv_attend.hpp"
+
+namespace kmkv {
+namespace {
+
+template <class T>
+__device__ __forceinline__ f32x4_t mfma16(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c) {
+  if constexpr (T::kExp == BF16::kExp)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
+}
+
+// One step's keys and values of a wavefront: 32 keys.
+template <int DP, bool LW>
+struct Tile {
+  u32x4_t k[2][DP / 32];
+  uint32_t v[8][DP / 32];  // 8 keys x DP / 16 columns
+  f32x4_t w[LW ? 2 : 1];
+  bool ok[2];              // (uniform) the halves' pages are in the cache
+};
+
+template <class T, int DP, int NQ, bool LW>
+struct Decode {
+  static constexpr int BM = 16 * NQ, KB = DP / 32, DV = DP / 16, VW = DP / 32;
+  static constexpr int LS = DP + 4;  // LDS row of a wavefront's partial result, in floats
+
+  static __device__ __forceinline__ void load(const AttendArgs& a, const int32_t* row, int head, int k, int lane,
+                                              Tile<DP, LW>& t) {
+    const int x = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int key = __builtin_amdgcn_readfirstlane(k + 16 * h);
+      const int page = page_of(a, row, key, t.ok[h]);
+      const int off = key & ((1 << a.page_shift) - 1);
+      const uint8_t* kp = a.k + page * a.k_page + off * a.k_slot + head * a.k_head + (x * a.k_slot + g * 16);
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        if (kb * 32 + g * 8 < a.D)
+          t.k[h][kb] = *(const u32x4_t*)(kp + kb * 64);
+        else
+          t.k[h][kb] = u32x4_t{0u, 0u, 0u, 0u};
+      }
+      if (LW) t.w[h] = *(const f32x4_t*)(a.lw + page * a.lw_page + head * a.lw_head + off + 4 * g);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int key = __builtin_amdgcn_readfirstlane(k + 16 * h);
+      bool ok;
+      const int page = page_of(a, row, key, ok);
+      const int off = key & ((1 << a.page_shift) - 1);
+      const uint8_t* vp = a.v + page * a.v_page + off * a.v_slot + head * a.v_head + (4 * g * a.v_slot + x * (DV * 2));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t* d = t.v[4 * h + j];
+        const uint8_t* s = vp + j * a.v_slot;
+        if constexpr (DP == 64) {
+          u32x2_t w = {0u, 0u};
+          if (x * DV < a.D) w = *(const u32x2_t*)s;
+          d[0] = w[0];
+          d[1] = w[1];
+        } else {
+#pragma unroll
+          for (int c = 0; c < VW; c += 4) {
+            u32x4_t w = {0u, 0u, 0u, 0u};
+            if (x * DV + 2 * c < a.D) w = *(const u32x4_t*)(s + 4 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[c + i] = w[i];
+          }
+        }
+      }
+    }
+  }
+};
+
+template <class T, int DP, int NQ, bool LW, bool PF>
+__global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void decode_kernel(AttendArgs a) {
+  using W = Decode<T, DP, NQ, LW>;
+  constexpr int BM = W::BM, KB = W::KB, DV = W::DV, LS = W::LS;
+  __shared__ int64_t scratch[16];
+  __shared__ float s_ml[4][BM][2];
+  __shared__ __align__(16) float s_o[4][BM][LS];
+  const int head = blockIdx.x % a.Hkv, it = blockIdx.x / a.Hkv;
+  Item w;
+  if (!find_item<BM, kDecodeUnit>(a, it, w, scratch)) return;
+  const int tid = threadIdx.x, lane = tid & 63, x = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rows = w.q.n * a.G, c = w.q.c;
+  if (head == 0 && w.split == 0)
+    for (int i = tid; i < w.q.n; i += kWgThreads) a.info[w.q.q0 + i] = make_int4(w.part0, w.splits, i, 0);
+  int k0, k1;
+  key_range<BM, kDecodeUnit>(a, w, k0, k1);
+  const int32_t* row = a.table + w.r * a.table_stride;
+
+  // queries: this lane's column of each group of 16 rows
+  u32x4_t qf[NQ][KB];
+  int jmin[NQ], jmax[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    const int m = min(16 * q + x, rows - 1);
+    const int i = m / a.G, hq = head * a.G + (m - i * a.G);
+    const uint16_t* qp = a.q + (int64_t)(w.q.q0 + i) * a.q_token + hq * a.q_head + g * 8;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      qf[q][kb] = u32x4_t{0u, 0u, 0u, 0u};
+      if (kb * 32 + g * 8 < a.D) qf[q][kb] = *(const u32x4_t*)(qp + kb * 32);
+    }
+    jmax[q] = min(c + i, k1 - 1);
+    jmin[q] = a.window > 0 ? c + i - a.window + 1 : 0;
+  }
+  // a step whose keys all rows see: from `full0`, up to `full1`
+  const int full1 = min(c + 1, k1), full0 = a.window > 0 ? c + w.q.n - a.window : 0;
+
+  f32x4_t o[NQ][DV];
+  float m_[NQ], l_[NQ];
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    m_[q] = -INFINITY;
+    l_[q] = 0.f;
+#pragma unroll
+    for (int e = 0; e < DV; ++e) o[q][e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+
+  auto process = [&](Tile<DP, LW>& t, int k) {
+    const bool all = k >= full0 && k + 32 <= full1 && t.ok[0] && t.ok[1];
+    bool odd = false;
+    if (!all || LW) {
+      // values of keys that no row sees are taken out, whatever they are
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int key = k + (j < 4 ? 0 : 16) + 4 * g + (j & 3);
+        bool in = (j < 4 ? t.ok[0] : t.ok[1]) && key < k1;
+        if (LW) in = in && t.w[j >> 2][j & 3] != -INFINITY;
+#pragma unroll
+        for (int i = 0; i < W::VW; ++i) {
+          if (!in) t.v[j][i] = 0u;
+          if (!all) odd |= odd_pair<T>(t.v[j][i]);
+        }
+      }
+      odd = __any(odd);
+      // rows differ in what they see and a value is infinite or NaN: take it
+      // out of the product and add it below to the rows that see it
+      if (odd) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < W::VW; ++i) t.v[j][i] = even_pair<T>(t.v[j][i]);
+      }
+    }
+    u32x4_t pf[NQ];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float s[8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) acc = mfma16<T>(t.k[h][kb], qf[q][kb], acc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v = acc[i] * a.scale;
+          if (LW) v = t.w[h][i] == -INFINITY ? -INFINITY : v + t.w[h][i];  // (whatever the key is)
+          s[4 * h + i] = v;
+        }
+      }
+      if (!all) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int key = k + (j < 4 ? 0 : 16) + 4 * g + (j & 3);
+          const bool see = (j < 4 ? t.ok[0] : t.ok[1]) && key >= jmin[q] && key <= jmax[q];
+          s[j] = see ? s[j] : -INFINITY;
+        }
+      }
+      float mx = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
+      mx = max16(max32(mx));
+      const float mn = fmaxf(m_[q], mx);
+      const float ms = mn == -INFINITY ? 0.f : mn;
+      const float al = factor<LW>(m_[q], ms);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[j] = factor<LW>(s[j], ms);
+        sum += s[j];
+      }
+      m_[q] = mn;
+      l_[q] = l_[q] * al + sum;
+#pragma unroll
+      for (int e = 0; e < DV; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[q][e][i] *= al;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pf[q][j] = T::pack(s[2 * j], s[2 * j + 1]);
+    }
+#pragma unroll
+    for (int e = 0; e < DV; ++e) {
+      u32x4_t vf;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        vf[j] = __builtin_amdgcn_perm(t.v[2 * j + 1][e / 2], t.v[2 * j][e / 2], e & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) o[q][e] = mfma16<T>(vf, pf[q], o[q][e]);
+    }
+    if (odd) {
+#pragma unroll 1
+      for (int key = k; key < min(k + 32, k1); ++key) {
+        bool ok;
+        const int page = page_of(a, row, key, ok);
+        const int off = key & ((1 << a.page_shift) - 1);
+        if (!ok || (LW && a.lw[page * a.lw_page + head * a.lw_head + off] == -INFINITY)) continue;
+        const uint16_t* vp = (const uint16_t*)(a.v + page * a.v_page + off * a.v_slot + head * a.v_head);
+#pragma unroll
+        for (int e = 0; e < DV; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int d = DV * (4 * g + i) + e;
+            const uint32_t v = d < a.D ? vp[d] : 0u;
+            if ((v & T::kExp) == T::kExp) {
+#pragma unroll
+              for (int q = 0; q < NQ; ++q)
+                if (key >= jmin[q] && key <= jmax[q]) o[q][e][i] += T::lo(v);
+            }
+          }
+      }
+    }
+  };
+
+  int k = k0 + 32 * wave;
+  if constexpr (PF) {
+    if (k < k1) {
+      Tile<DP, LW> ta, tb;
+      W::load(a, row, head, k, lane, ta);
+      for (;;) {
+        if (k + kDecodeUnit < k1) W::load(a, row, head, k + kDecodeUnit, lane, tb);
+        process(ta, k);
+        k += kDecodeUnit;
+        if (k >= k1) break;
+        if (k + kDecodeUnit < k1) W::load(a, row, head, k + kDecodeUnit, lane, ta);
+        process(tb, k);
+        k += kDecodeUnit;
+        if (k >= k1) break;
+      }
+    }
+  } else {
+    for (; k < k1; k += kDecodeUnit) {
+      Tile<DP, LW> t;
+      W::load(a, row, head, k, lane, t);
+      process(t, k);
+    }
+  }
+
+  // Join the four wavefronts.
+#pragma unroll
+  for (int q = 0; q < NQ; ++q) {
+    const float l = sum16(sum32(l_[q]));
+    if (g == 0) {
+      s_ml[wave][16 * q + x][0] = m_[q];
+      s_ml[wave][16 * q + x][1] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < DV; e += 4)
+        *(f32x4_t*)&s_o[wave][16 * q + x][DV * (4 * g + i) + e] =
+            f32x4_t{o[q][e][i], o[q][e + 1][i], o[q][e + 2][i], o[q][e + 3][i]};
+  }
+  __syncthreads();
+  constexpr int PR = DP / 4;  // 16-byte pieces of a row
+  for (int p = tid; p < BM * PR; p += kWgThreads) {
+    const int m = p / PR, d = (p - m * PR) * 4;
+    if (m >= rows) break;
+    float M = fmaxf(fmaxf(s_ml[0][m][0], s_ml[1][m][0]), fmaxf(s_ml[2][m][0], s_ml[3][m][0]));
+    const float ms = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float f = factor<LW>(s_ml[v][m][0], ms);
+      L += f * s_ml[v][m][1];
+      const f32x4_t ov = *(const f32x4_t*)&s_o[v][m][d];
+      if (s_ml[v][m][0] != -INFINITY) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += f * ov[i];
+      }
+    }
+    if (w.splits == 1) {
+      const int i = m / a.G, hq = head * a.G + (m - i * a.G);
+      const int64_t tok = w.q.q0 + i;
+      const float inv = L == 0.f ? 0.f : 1.0f / L;
+      if (d < a.D)
+        *(u32x2_t*)(a.out + tok * a.o_token + hq * a.o_head + d) =
+            u32x2_t{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
+      if (a.lse && d == 0) a.lse[tok * a.Hq + hq] = log_sum<LW>(ms, L);
+    } else {
+      const int64_t at = ((int64_t)w.part() * a.Hkv + head) * BM + m;
+      *(f32x4_t*)(a.part_o + at * DP + d) = acc;
+      if (d == 0) a.part_ml[at] = f32x2_t{M, L};
+    }
+  }
+}
+
+// out = sum over the parts of e^(m - M) o, divided by that of l.  One thread
+// per 4 columns of a row.
+template <class T, int DP, bool LW>
+__global__ __launch_bounds__(kWgThreads) void join_kernel(JoinArgs a) {
+  const int t = blockIdx.x;
+  if (t >= min(a.query_start[a.R], a.T)) return;
+  const int4 f = a.info[t];
+  const bool chunk = f.w != 0;
+  const int bm = chunk ? kChunkRows : a.bm0, parts = chunk ? a.parts1 : a.parts0;
+  if (f.y <= 1) return;
+  const float* po = chunk ? a.o1 : a.o0;
+  const f32x2_t* pml = chunk ? a.ml1 : a.ml0;
+  constexpr int PR = DP / 4;
+  const int p = blockIdx.y * kWgThreads + threadIdx.x;
+  const int hq = p / PR, d = (p - hq * PR) * 4;
+  if (hq >= a.Hq || d >= a.D) return;
+  const int head = hq / a.G;
+  const int64_t m = (int64_t)f.z * a.G + (hq - head * a.G);
+  const int64_t tile = m / bm, first = f.x + tile * f.y;
+  if (f.x < 0 || f.z < 0 || first + f.y > parts) return;  // (no such part: more new tokens than max_new)
+  const int64_t at = (first * a.Hkv + head) * bm + (m - tile * bm), step = (int64_t)a.Hkv * bm;
+  float M = -INFINITY;
+  for (int s = 0; s < f.y; ++s) M = fmaxf(M, pml[at + s * step][0]);
+  const float ms = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < f.y; ++s) {
+    const f32x2_t ml = pml[at + s * step];
+    const float w = factor<LW>(ml[0], ms);
+    L += w * ml[1];
+    if (ml[0] == -INFINITY) continue;  // (a part that saw nothing wrote no o)
+    const f32x4_t ov = *(const f32x4_t*)(po + (at + s * step) * DP + d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] += w * ov[i];
+  }
+  const float inv = L == 0.f ? 0.f : 1.0f / L;
+  *(u32x2_t*)(a.out + t * a.o_token + hq * a.o_head + d) =
+      u32x2_t{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
+  if (a.lse && d == 0) a.lse[(int64_t)t * a.Hq + hq] = log_sum<LW>(ms, L);
+}
+
+template <class T, int DP, int NQ>
+void decode_lw(const AttendArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((int64_t)a.max_items * a.Hkv));
+  constexpr bool PF = DP <= 128;
+  if (a.lw)
+    decode_kernel<T, DP, NQ, true, PF><<<grid, kWgThreads, 0, stream>>>(a);
+  else
+    decode_kernel<T, DP, NQ, false, PF><<<grid, kWgThreads, 0, stream>>>(a);
+}
+
+template <class T, int NQ>
+void decode_dim(const AttendArgs& a, hipStream_t stream) {
+  const int dp = dim_pad(a.D);
+  if (dp == 64)
+    decode_lw<T, 64, NQ>(a, stream);
+  else if (dp == 128)
+    decode_lw<T, 128, NQ>(a, stream);
+  else
+    decode_lw<T, 256, NQ>(a, stream);
+}
+
+template <class T, bool LW>
+void join_dim(const JoinArgs& a, hipStream_t stream) {
+  const int dp = dim_pad(a.D);
+  const dim3 grid((unsigned)a.T, (unsigned)(((int64_t)a.Hq * (dp / 4) + kWgThreads - 1) / kWgThreads));
+  if (dp == 64)
+    join_kernel<T, 64, LW><<<grid, kWgThreads, 0, stream>>>(a);
+  else if (dp == 128)
+    join_kernel<T, 128, LW><<<grid, kWgThreads, 0, stream>>>(a);
+  else
+    join_kernel<T, 256, LW><<<grid, kWgThreads, 0, stream>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_decode(const AttendArgs& a, int dt, int bm, hipStream_t stream) {
+  if (dt == 1)
+    bm == 16 ? decode_dim<BF16, 1>(a, stream) : decode_dim<BF16, 2>(a, stream);
+  else
+    bm == 16 ? decode_dim<F16, 1>(a, stream) : decode_dim<F16, 2>(a, stream);
+  return hipGetLastError();
+}
+
+hipError_t launch_join(const JoinArgs& a, int dt, hipStream_t stream) {
+  if (dt == 1)
+    a.weighted ? join_dim<BF16, true>(a, stream) : join_dim<BF16, false>(a, stream);
+  else
+    a.weighted ? join_dim<F16, true>(a, stream) : join_dim<F16, false>(a, stream);
+  return hipGetLastError();
+}
+
+}  // namespace kmkv
