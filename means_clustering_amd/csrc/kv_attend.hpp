@@ -148,6 +148,16 @@ __device__ __forceinline__ int page_of(const AttendArgs& a, const int32_t* row, 
   ok = p >= 0 && p < a.pages;
   return ok ? p : 0;
 }
+// The same for a key that is uniform over the wavefront: a scalar load (the
+// kernels do not write the table), which does not wait for the vector loads
+// in flight.
+__device__ __forceinline__ int page_of_uniform(const AttendArgs& a, const int32_t* row, int key, bool& ok) {
+  typedef const __attribute__((address_space(4))) int32_t* table_t;
+  const int col = __builtin_amdgcn_readfirstlane(key) >> a.page_shift;
+  const int p = col < a.width ? ((table_t)(uintptr_t)row)[col] : -1;
+  ok = p >= 0 && p < a.pages;
+  return ok ? p : 0;
+}
 
 // Largest and sum over the lanes l, l ^ 32 (and l ^ 16).
 __device__ __forceinline__ float max32(float x) {

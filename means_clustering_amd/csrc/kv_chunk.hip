@@ -21,10 +21,14 @@
 // LDS rows are DP elements; their 16-byte pieces are permuted by an exclusive
 // or with the row, so that the reads of K (8 rows, one piece column) and of V
 // (4 rows, 2 neighbouring pieces) meet no bank twice.
+#include <type_traits>
+
 #include "kv_attend.hpp"
 
 namespace kmkv {
 namespace {
+
+constexpr int kLoadsDone = 0x0f70;  // s_waitcnt vmcnt(0)
 
 template <class T>
 __device__ __forceinline__ f32x16_t mfma32(const u32x4_t& a, const u32x4_t& b, const f32x16_t& c) {
@@ -39,17 +43,17 @@ __device__ __forceinline__ f32x16_t mfma32(const u32x4_t& a, const u32x4_t& b, c
 template <class T, int DP, bool LW>
 __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(AttendArgs a) {
   constexpr int BM = kChunkRows, BN = chunk_unit(DP);
-  constexpr int KB = DP / 16;              // depth steps of K Q'
-  constexpr int CH = DP / 8;               // 16-byte pieces of an LDS row
-  constexpr int RP = kWgThreads / CH;      // rows staged by one round of the workgroup
-  constexpr int ROUNDS = BN / RP;
+  constexpr int KB = DP / 16;           // depth steps of K Q'
+  constexpr int CH = DP / 8;            // 16-byte pieces of an LDS row
+  constexpr int WR = BN / 4;            // rows of a tile that a wavefront copies
+  constexpr int NI = WR * CH / 64;      // ... in this many instructions of 64 pieces
   constexpr int NT = BN / 32, DT = DP / 32;
+  constexpr int TP = BN * CH;           // pieces of a tile
   __shared__ int64_t scratch[16];
-  __shared__ __align__(16) u32x4_t s_k[2][BN * CH];
-  __shared__ __align__(16) u32x4_t s_v[2][BN * CH];
+  __shared__ __align__(16) u32x4_t s_k[2 * TP];
+  __shared__ __align__(16) u32x4_t s_v[2 * TP];
   __shared__ __align__(16) float s_w[2][LW ? BN : 4];
-  // first key of the buffer's tile if it holds an infinite or NaN value (taken out), or lies partly in no page
-  __shared__ int s_odd[2], s_bad[2];
+  __shared__ int s_odd;  // a value was infinite or NaN in a tile that not all rows see, and taken out
   const int head = blockIdx.x % a.Hkv, it = blockIdx.x / a.Hkv;
   Item w;
   if (!find_item<BM, BN>(a, it, w, scratch)) return;
@@ -62,17 +66,20 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
   int k0, k1;
   key_range<BM, BN>(a, w, k0, k1);
   const int32_t* row = a.table + w.r * a.table_stride;
+  const int pmask = (1 << a.page_shift) - 1;
 
   // this lane's query row
   const int m = w.tile * BM + 32 * wave + x, mc = min(m, rows - 1);
   const int qi = mc / a.G, hq = head * a.G + (mc - qi * a.G);
+  const float scale = fmaxf(fabsf(a.scale), 1e-30f);  // (above 0, so that the largest product is the largest score)
   u32x4_t qf[KB];
   {
     const uint16_t* qp = a.q + (int64_t)(w.q.q0 + qi) * a.q_token + hq * a.q_head + 8 * h;
+    const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       qf[kb] = u32x4_t{0u, 0u, 0u, 0u};
-      if (16 * kb + 8 * h < a.D) qf[kb] = *(const u32x4_t*)(qp + 16 * kb);
+      if (16 * kb + 8 * h < a.D) qf[kb] = *(const u32x4_t*)(qp + 16 * kb) ^ sign;
     }
   }
   const int jmax = min(c + qi, k1 - 1), jmin = a.window > 0 ? c + qi - a.window + 1 : 0;
@@ -91,185 +98,234 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   float m_ = -INFINITY, l_ = 0.f;
 
-  // staging: this thread's piece of a row, ROUNDS rows
-  const int sc = tid % CH, sr = tid / CH;
-  u32x4_t rk[ROUNDS], rv[ROUNDS];
-  bool rok[ROUNDS];
-  float rw = 0.f;
-  bool bad = false;
-  auto load = [&](int kt) {
-    bad = false;
+  // Are all pages of the item's keys in the cache?  (Uniform.)
+  bool hole = false;
+  for (int j = (k0 & ~pmask) + (tid << a.page_shift); j < k1; j += kWgThreads << a.page_shift) {
+    bool ok;
+    (void)page_of(a, row, j, ok);
+    hole |= !ok;
+  }
+  const bool holes = __syncthreads_or(hole);
+  if (a.D < DP) {  // pieces beyond the rows' end are not copied
+    for (int i = tid; i < 2 * TP; i += kWgThreads) s_k[i] = s_v[i] = u32x4_t{0u, 0u, 0u, 0u};
+  }
+  if (tid == 0) s_odd = 0;
+  __syncthreads();
+
+  // Copies of a tile: the wavefront's rows lie in one page.
+  auto page_at = [&](int kt) __attribute__((always_inline)) {
+    bool ok;
+    return page_of_uniform(a, row, kt + wave * WR, ok);
+  };
+  auto copy_rows = [&](int kt, int page, int buf, bool whole) __attribute__((always_inline)) {
+    const int off = (kt + wave * WR) & pmask;
+    const uint8_t* kp = a.k + page * a.k_page + head * a.k_head + off * a.k_slot;
+    const uint8_t* vp = a.v + page * a.v_page + head * a.v_head + off * a.v_slot;
 #pragma unroll
-    for (int i = 0; i < ROUNDS; ++i) {
-      // a wavefront's rows of a round lie in one page
-      const int key0 = __builtin_amdgcn_readfirstlane(kt + i * RP + (wave * 64) / CH);
-      bool ok;
-      const int page = page_of(a, row, key0, ok);
-      const int key = kt + i * RP + sr, off = key & ((1 << a.page_shift) - 1);
-      rok[i] = ok && key < k1;
-      bad |= !ok && key0 < k1;
-      rk[i] = rv[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (8 * sc < a.D) {
-        rk[i] = *(const u32x4_t*)(a.k + page * a.k_page + head * a.k_head + (off * a.k_slot + sc * 16));
-        rv[i] = *(const u32x4_t*)(a.v + page * a.v_page + head * a.v_head + (off * a.v_slot + sc * 16));
-      }
-      if (LW) {
-        const float lw = a.lw[page * a.lw_page + head * a.lw_head + off];
-        rok[i] = rok[i] && lw != -INFINITY;
-      }
-    }
-    if (LW && tid < BN) {
-      bool ok;
-      const int page = page_of(a, row, kt + tid, ok);
-      rw = ok ? a.lw[page * a.lw_page + head * a.lw_head + ((kt + tid) & ((1 << a.page_shift) - 1))] : -INFINITY;
+    for (int i = 0; i < NI; ++i) {
+      const int r = i * (64 / CH) + lane / CH, pc = lane % CH;  // row of the wavefront's, piece of the LDS row
+      const int at = buf * TP + (wave * NI + i) * 64;
+      const int kr = wave * WR + r;
+      const int kc = pc ^ (kr & 7), vc = pc ^ ((2 * kr) & (CH - 1) & 14);
+      if (whole || 8 * kc < a.D)
+        __builtin_amdgcn_global_load_lds((const void*)(kp + (r * a.k_slot + kc * 16)),
+                                         (__attribute__((address_space(3))) void*)(s_k + at), 16, 0, 0);
+      if (whole || 8 * vc < a.D)
+        __builtin_amdgcn_global_load_lds((const void*)(vp + (r * a.v_slot + vc * 16)),
+                                         (__attribute__((address_space(3))) void*)(s_v + at), 16, 0, 0);
     }
   };
-  auto store = [&](int kt, int buf) {
-    const bool part = kt < wfull0 || kt + BN > wfull1;
+  auto copy = [&](int kt, int page, int buf) __attribute__((always_inline)) {
+    if (a.D == DP)
+      copy_rows(kt, page, buf, true);
+    else
+      copy_rows(kt, page, buf, false);
+  };
+  // Weights of a tile, one for each of the first BN threads.
+  auto weight_at = [&](int kt) __attribute__((always_inline)) {
+    bool ok;
+    const int key = kt + tid, page = page_of(a, row, key, ok);
+    const float v = a.lw[page * a.lw_page + head * a.lw_head + (key & pmask)];
+    return ok && key < k1 ? v : -INFINITY;
+  };
+  // Takes out of the staged values what no row sees, whatever it is, and in a tile that not all rows see (`part`)
+  // what is infinite or NaN.
+  auto clean = [&](int kt, int buf, bool part) __attribute__((always_inline)) {
     bool odd = false;
-#pragma unroll
-    for (int i = 0; i < ROUNDS; ++i) {
+    for (int i = tid; i < TP; i += kWgThreads) {
+      const int r = i / CH, key = kt + r;
+      bool in = key < k1;
+      if (holes) {
+        bool ok;
+        (void)page_of(a, row, key, ok);
+        in = in && ok;
+      }
+      if (LW) in = in && s_w[buf][r] != -INFINITY;
+      if (!part && in) continue;
+      u32x4_t v = s_v[buf * TP + i];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        // values (and, for the sake of their products, keys) that no row sees are taken out, whatever they are
-        if (!rok[i]) rk[i][j] = rv[i][j] = 0u;
-        if (part) odd |= odd_pair<T>(rv[i][j]);
+        if (!in) v[j] = 0u;
+        odd |= odd_pair<T>(v[j]);
+        v[j] = even_pair<T>(v[j]);
       }
+      s_v[buf * TP + i] = v;
     }
-    if (part && __any(odd)) {
-#pragma unroll
-      for (int i = 0; i < ROUNDS; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) rv[i][j] = even_pair<T>(rv[i][j]);
-      if (lane == 0) s_odd[buf] = kt;
-    }
-#pragma unroll
-    for (int i = 0; i < ROUNDS; ++i) {
-      const int r = i * RP + sr;
-      s_k[buf][r * CH + (sc ^ (r & 7))] = rk[i];
-      s_v[buf][r * CH + (sc ^ ((2 * r) & (CH - 1) & 14))] = rv[i];
-    }
-    if (bad && lane == 0) s_bad[buf] = kt;
-    if (LW && tid < BN) s_w[buf][tid] = rw;
+    if (odd) s_odd = 1;
   };
 
-  if (tid < 2) s_odd[tid] = s_bad[tid] = -1;
-  __syncthreads();
-  if (k0 < k1) {
-    load(k0);
-    store(k0, 0);
+  // LDS addresses of this lane's operands: K's piece 2 kb + h of row x, V's 4 rows of 16 columns for each 32 columns
+  int ka[KB], va[DT];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) ka[kb] = x * CH + ((2 * kb + h) ^ (x & 7));
+  {
+    const int r = 4 * h + ((lane & 15) >> 2);
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const int col = 32 * d + ((lane >> 4) & 1) * 16 + 4 * (lane & 3);  // elements
+      va[d] = (r * CH + ((col >> 3) ^ ((2 * r) & (CH - 1) & 14))) * 16 + (col & 4) * 2;
+    }
   }
-  __syncthreads();
-  int buf = 0;
-  for (int kt = k0; kt < k1; kt += BN, buf ^= 1) {
-    const bool more = kt + BN < k1;
-    if (more) load(kt + BN);
-    if (kt + BN > see0 && kt < see1) {
-      f32x16_t s[NT];
+
+  auto multiply = [&](int kt, int buf) __attribute__((always_inline)) {
+    f32x16_t s[NT];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[t][i] = 0.f;
+      for (int i = 0; i < 16; ++i) s[t][i] = 0.f;
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          const int r = 32 * t + x;
-          s[t] = mfma32<T>(s_k[buf][r * CH + ((2 * kb + h) ^ (r & 7))], qf[kb], s[t]);
-        }
-      }
+      for (int kb = 0; kb < KB; ++kb) s[t] = mfma32<T>(s_k[buf * TP + 32 * t * CH + ka[kb]], qf[kb], s[t]);
+    }
+    if (LW) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          f32x4_t wv;
-          if (LW) wv = *(const f32x4_t*)&s_w[buf][32 * t + 8 * b + 4 * h];
+          const f32x4_t wv = *(const f32x4_t*)&s_w[buf][32 * t + 8 * b + 4 * h];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float v = s[t][4 * b + i] * a.scale;
-            if (LW) v = wv[i] == -INFINITY ? -INFINITY : v + wv[i];
-            s[t][4 * b + i] = v;
+            const float v = s[t][4 * b + i] * scale + wv[i];
+            s[t][4 * b + i] = wv[i] == -INFINITY ? -INFINITY : v;  // (whatever the key is)
           }
         }
-      const bool holes = s_bad[buf] == kt;
-      if (kt < full0 || kt + BN > full1 || holes) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int key = kt + 32 * t + 8 * (i / 4) + 4 * h + (i & 3);
-            bool see = key >= jmin && key <= jmax;
-            if (holes && see) (void)page_of(a, row, key, see);
-            s[t][i] = see ? s[t][i] : -INFINITY;
-          }
+    }
+    if (kt < full0 || kt + BN > full1 || holes) {
+      uint32_t held = ~0u;  // bit g: keys 16 g .. 16 g + 15 of the tile lie in a page of the cache
+      if (holes) {
+#pragma unroll 1
+        for (int g = 0; g < BN / 16; ++g) {
+          bool ok;
+          (void)page_of_uniform(a, row, kt + 16 * g, ok);
+          if (!ok) held &= ~(1u << g);
+        }
       }
-      float mx = -INFINITY;
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
-      mx = max32(mx);
-      const float mn = fmaxf(m_, mx), ms = mn == -INFINITY ? 0.f : mn;
-      if (__any(mn > m_)) {
-        const float al = factor<LW>(m_, ms);
-        l_ *= al;
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[d][i] *= al;
-        m_ = mn;
-      }
-      float sum = 0.f;
+      const int from = jmin - kt - 4 * h, upto = jmax - kt - 4 * h;
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          s[t][i] = factor<LW>(s[t][i], ms);
-          sum += s[t][i];
+          const int j = 32 * t + 8 * (i / 4) + (i & 3);
+          const bool see = j >= from && j <= upto && ((held >> (2 * t + i / 8)) & 1);
+          s[t][i] = see ? s[t][i] : -INFINITY;
         }
-      l_ += sum;
+    }
+    float mx = s[0][0];
 #pragma unroll
-      for (int u = 0; u < 2 * NT; ++u) {
-        u32x4_t pf;
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pf[j] = T::pack(s[u / 2][8 * (u & 1) + 2 * j], s[u / 2][8 * (u & 1) + 2 * j + 1]);
+      for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
+    mx = max32(mx);
+    if (!LW) mx *= scale;
+    const float mn = fmaxf(m_, mx), ms = mn == -INFINITY ? 0.f : mn;
+    if (__any(mn > m_)) {
+      const float al = factor<LW>(m_, ms);
+      l_ *= al;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const int r = 16 * u + 4 * h + ((lane & 15) >> 2);
-          const int col = 32 * d + ((lane >> 4) & 1) * 16 + 4 * (lane & 3);  // elements
-          u32x4_t vf;
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int re = r + 8 * e;
-            const char* at = (const char*)&s_v[buf][re * CH + ((col >> 3) ^ ((2 * re) & (CH - 1) & 14))] + (col & 4) * 2;
-            const s16x4_t tr = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) s16x4_t*)(__attribute__((address_space(3))) char*)at);
-            const u32x2_t two = __builtin_bit_cast(u32x2_t, tr);
-            vf[2 * e] = two[0];
-            vf[2 * e + 1] = two[1];
-          }
-          o[d] = mfma32<T>(vf, pf, o[d]);
-        }
+        for (int i = 0; i < 16; ++i) o[d][i] *= al;
+      m_ = mn;
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[t][i] = LW ? factor<LW>(s[t][i], ms) : exp2_(fmaf(s[t][i], scale, -ms));
+        sum += s[t][i];
       }
-      if (s_odd[buf] == kt) {
-#pragma unroll 1
-        for (int key = kt; key < min(kt + BN, k1); ++key) {
-          bool ok;
-          const int page = page_of(a, row, key, ok);
-          const int off = key & ((1 << a.page_shift) - 1);
-          if (!ok || (LW && a.lw[page * a.lw_page + head * a.lw_head + off] == -INFINITY)) continue;
-          const uint16_t* vp = (const uint16_t*)(a.v + page * a.v_page + off * a.v_slot + head * a.v_head);
+    l_ += sum;
 #pragma unroll
-          for (int d = 0; d < DT; ++d)
+    for (int u = 0; u < 2 * NT; ++u) {
+      u32x4_t pf;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int e = 32 * d + 8 * (i / 4) + 4 * h + (i & 3);
-              const uint32_t v = e < a.D ? vp[e] : 0u;
-              if ((v & T::kExp) == T::kExp && key >= jmin && key <= jmax) o[d][i] += T::lo(v);
-            }
+      for (int j = 0; j < 4; ++j) pf[j] = T::pack(s[u / 2][8 * (u & 1) + 2 * j], s[u / 2][8 * (u & 1) + 2 * j + 1]);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        u32x4_t vf;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const char* at = (const char*)s_v + va[d] + (buf * TP + (16 * u + 8 * e) * CH) * 16;
+          const u32x2_t two = __builtin_bit_cast(
+              u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)at));
+          vf[2 * e] = two[0];
+          vf[2 * e + 1] = two[1];
         }
+        o[d] = mfma32<T>(vf, pf, o[d]);
       }
     }
-    if (more) store(kt + BN, buf ^ 1);
+  };
+
+  int page = 0;
+  if (k0 < k1) {
+    copy(k0, page_at(k0), 0);
+    if (LW && tid < BN) s_w[0][tid] = weight_at(k0);
+    page = page_at(k0 + BN);
+  }
+  __builtin_amdgcn_s_waitcnt(kLoadsDone);
+  __syncthreads();
+  // One tile: the next is copied to the other buffer meanwhile.
+  auto step = [&](int kt, auto b) __attribute__((always_inline)) {
+    constexpr int buf = decltype(b)::value;
+    const bool more = kt + BN < k1;
+    float wn = 0.f;
+    if (more) {
+      copy(kt + BN, page, buf ^ 1);
+      page = page_at(kt + 2 * BN);
+      if (LW && tid < BN) wn = weight_at(kt + BN);
+    }
+    if (LW || holes || kt < wfull0 || kt + BN > wfull1) {
+      clean(kt, buf, kt < wfull0 || kt + BN > wfull1);
+      __syncthreads();
+    }
+    if (kt + BN > see0 && kt < see1) multiply(kt, buf);
+    if (LW && more && tid < BN) s_w[buf ^ 1][tid] = wn;
+    __builtin_amdgcn_s_waitcnt(kLoadsDone);
     __syncthreads();
+  };
+  for (int kt = k0; kt < k1; kt += 2 * BN) {
+    step(kt, std::integral_constant<int, 0>{});
+    if (kt + BN < k1) step(kt + BN, std::integral_constant<int, 1>{});
+  }
+
+  if (s_odd) {  // the values taken out, added to the rows that see them
+#pragma unroll 1
+    for (int key = k0; key < k1; ++key) {
+      const int kt = key - key % BN;
+      if (kt >= wfull0 && kt + BN <= wfull1) continue;  // (all rows see this tile: nothing was taken out)
+      bool ok;
+      const int page = page_of_uniform(a, row, key, ok), off = key & pmask;
+      if (!ok || (LW && a.lw[page * a.lw_page + head * a.lw_head + off] == -INFINITY)) continue;
+      const uint16_t* vp = (const uint16_t*)(a.v + page * a.v_page + off * a.v_slot + head * a.v_head);
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = 32 * d + 8 * (i / 4) + 4 * h + (i & 3);
+          const uint32_t v = e < a.D ? vp[e] : 0u;
+          if ((v & T::kExp) == T::kExp && key >= jmin && key <= jmax) o[d][i] += T::lo(v);
+        }
+    }
   }
 
   const float L = sum32(l_);

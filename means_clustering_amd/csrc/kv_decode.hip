@@ -40,7 +40,8 @@ struct Tile {
   u32x4_t k[2][DP / 32];
   uint32_t v[8][DP / 32];  // 8 keys x DP / 16 columns
   f32x4_t w[LW ? 2 : 1];
-  bool ok[2];              // (uniform) the halves' pages are in the cache
+  int page[2];             // (uniform) the halves' pages
+  bool ok[2];              // ... are in the cache
 };
 
 template <class T, int DP, int NQ, bool LW>
@@ -53,8 +54,9 @@ struct Decode {
     const int x = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int key = __builtin_amdgcn_readfirstlane(k + 16 * h);
-      const int page = page_of(a, row, key, t.ok[h]);
+      const int key = k + 16 * h;
+      t.page[h] = page_of_uniform(a, row, key, t.ok[h]);
+      const int64_t page = t.page[h];
       const int off = key & ((1 << a.page_shift) - 1);
       const uint8_t* kp = a.k + page * a.k_page + off * a.k_slot + head * a.k_head + (x * a.k_slot + g * 16);
 #pragma unroll
@@ -68,9 +70,8 @@ struct Decode {
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int key = __builtin_amdgcn_readfirstlane(k + 16 * h);
-      bool ok;
-      const int page = page_of(a, row, key, ok);
+      const int key = k + 16 * h;
+      const int64_t page = t.page[h];
       const int off = key & ((1 << a.page_shift) - 1);
       const uint8_t* vp = a.v + page * a.v_page + off * a.v_slot + head * a.v_head + (4 * g * a.v_slot + x * (DV * 2));
 #pragma unroll
@@ -144,7 +145,8 @@ __global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void de
     for (int e = 0; e < DV; ++e) o[q][e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
 
-  auto process = [&](Tile<DP, LW>& t, int k) {
+  bool some_odd = false;
+  auto process = [&](Tile<DP, LW>& t, int k) __attribute__((always_inline)) {
     const bool all = k >= full0 && k + 32 <= full1 && t.ok[0] && t.ok[1];
     bool odd = false;
     if (!all || LW) {
@@ -160,10 +162,10 @@ __global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void de
           if (!all) odd |= odd_pair<T>(t.v[j][i]);
         }
       }
-      odd = __any(odd);
       // rows differ in what they see and a value is infinite or NaN: take it
-      // out of the product and add it below to the rows that see it
-      if (odd) {
+      // out of the product and add it in the end to the rows that see it
+      if (__any(odd)) {
+        some_odd = true;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -223,28 +225,6 @@ __global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void de
 #pragma unroll
       for (int q = 0; q < NQ; ++q) o[q][e] = mfma16<T>(vf, pf[q], o[q][e]);
     }
-    if (odd) {
-#pragma unroll 1
-      for (int key = k; key < min(k + 32, k1); ++key) {
-        bool ok;
-        const int page = page_of(a, row, key, ok);
-        const int off = key & ((1 << a.page_shift) - 1);
-        if (!ok || (LW && a.lw[page * a.lw_page + head * a.lw_head + off] == -INFINITY)) continue;
-        const uint16_t* vp = (const uint16_t*)(a.v + page * a.v_page + off * a.v_slot + head * a.v_head);
-#pragma unroll
-        for (int e = 0; e < DV; ++e)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int d = DV * (4 * g + i) + e;
-            const uint32_t v = d < a.D ? vp[d] : 0u;
-            if ((v & T::kExp) == T::kExp) {
-#pragma unroll
-              for (int q = 0; q < NQ; ++q)
-                if (key >= jmin[q] && key <= jmax[q]) o[q][e][i] += T::lo(v);
-            }
-          }
-      }
-    }
   };
 
   int k = k0 + 32 * wave;
@@ -268,6 +248,30 @@ __global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void de
       Tile<DP, LW> t;
       W::load(a, row, head, k, lane, t);
       process(t, k);
+    }
+  }
+
+  if (some_odd) {
+#pragma unroll 1
+    for (int key = k0; key < k1; ++key) {
+      const int kt = key - key % 32;
+      if ((kt / 32) % 4 != wave || (kt >= full0 && kt + 32 <= full1)) continue;  // (not this wavefront's, or whole)
+      bool ok;
+      const int page = page_of_uniform(a, row, key, ok), off = key & ((1 << a.page_shift) - 1);
+      if (!ok || (LW && a.lw[page * a.lw_page + head * a.lw_head + off] == -INFINITY)) continue;
+      const uint16_t* vp = (const uint16_t*)(a.v + page * a.v_page + off * a.v_slot + head * a.v_head);
+#pragma unroll
+      for (int e = 0; e < DV; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int d = DV * (4 * g + i) + e;
+          const uint32_t v = d < a.D ? vp[d] : 0u;
+          if ((v & T::kExp) == T::kExp) {
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+              if (key >= jmin[q] && key <= jmax[q]) o[q][e][i] += T::lo(v);
+          }
+        }
     }
   }
 

@@ -407,6 +407,16 @@ def test_attend_unseen_values_do_not_reach_a_row(n, hq, bad, window):
                 assert bool(((out[t] - want[t]).abs() <= tol[t]).all()), t
 
 
+@pytest.mark.parametrize("n,hq", [(4, 4), (3, 8), (90, 4)])
+def test_attend_values_that_all_rows_see_beside_ones_that_some_do(n, hq):
+    """An infinite value just before the new tokens, in a tile that not all rows see whole, reaches every row."""
+    for back in (1, 2, 20):
+        c = Case([(150, n), (100, n)], hq, 2, 64, BF)
+        c.set(0, 150 - n - back, v=math.inf)
+        out = kvcache.attend(**c.device())
+        assert bool((out[:n] == math.inf).all()) and bool(torch.isfinite(out[n:]).all())
+
+
 @pytest.mark.parametrize("n", [1, 60])
 def test_attend_pages_outside_the_cache_are_not_seen(n):
     c = Case([(200, n), (90, n)], 4, 2, 128, BF, weighted=n == 60)
