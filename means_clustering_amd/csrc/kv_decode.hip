@@ -326,44 +326,80 @@ __global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void de
 }
 
 // out = sum over the parts of e^(m - M) o, divided by that of l.  One thread
-// per 4 columns of a row.
-template <class T, int DP, bool LW>
+// takes 4 columns of a row in every NG-th part, four parts at a time; NG such
+// threads are joined through LDS.
+template <class T, int DP, bool LW, int NG>
 __global__ __launch_bounds__(kWgThreads) void join_kernel(JoinArgs a) {
-  const int t = blockIdx.x;
-  if (t >= min(a.query_start[a.R], a.T)) return;
+  constexpr int PR = DP / 4, ROWS = kWgThreads / (PR * NG);
+  __shared__ __align__(16) float s_o[NG > 1 ? NG : 1][NG > 1 ? ROWS * PR : 1][4];
+  __shared__ float s_ml[NG > 1 ? NG : 1][NG > 1 ? ROWS : 1][2];
+  const int t = blockIdx.x, total = a.query_start[a.R];
   const int4 f = a.info[t];
+  if (t >= total || f.y <= 1) return;
   const bool chunk = f.w != 0;
   const int bm = chunk ? kChunkRows : a.bm0, parts = chunk ? a.parts1 : a.parts0;
-  if (f.y <= 1) return;
   const float* po = chunk ? a.o1 : a.o0;
   const f32x2_t* pml = chunk ? a.ml1 : a.ml0;
-  constexpr int PR = DP / 4;
-  const int p = blockIdx.y * kWgThreads + threadIdx.x;
-  const int hq = p / PR, d = (p - hq * PR) * 4;
-  if (hq >= a.Hq || d >= a.D) return;
-  const int head = hq / a.G;
-  const int64_t m = (int64_t)f.z * a.G + (hq - head * a.G);
+  const int p = threadIdx.x % (PR * ROWS), ng = threadIdx.x / (PR * ROWS);
+  const int hq = blockIdx.y * ROWS + p / PR, d = (p % PR) * 4;
+  const int head = min(hq, a.Hq - 1) / a.G;
+  const int64_t m = (int64_t)f.z * a.G + (min(hq, a.Hq - 1) - head * a.G);
   const int64_t tile = m / bm, first = f.x + tile * f.y;
   if (f.x < 0 || f.z < 0 || first + f.y > parts) return;  // (no such part: more new tokens than max_new)
   const int64_t at = (first * a.Hkv + head) * bm + (m - tile * bm), step = (int64_t)a.Hkv * bm;
-  float M = -INFINITY;
-  for (int s = 0; s < f.y; ++s) M = fmaxf(M, pml[at + s * step][0]);
-  const float ms = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
+  float M = -INFINITY, L = 0.f;
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < f.y; ++s) {
-    const f32x2_t ml = pml[at + s * step];
-    const float w = factor<LW>(ml[0], ms);
-    L += w * ml[1];
-    if (ml[0] == -INFINITY) continue;  // (a part that saw nothing wrote no o)
-    const f32x4_t ov = *(const f32x4_t*)(po + (at + s * step) * DP + d);
+  for (int s0 = ng; s0 < f.y; s0 += 4 * NG) {
+    f32x2_t ml[4];
+    f32x4_t ov[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] += w * ov[i];
+    for (int j = 0; j < 4; ++j) {
+      const int s = min(s0 + j * NG, f.y - 1);  // (the last part again, with no weight)
+      ml[j] = pml[at + s * step];
+      ov[j] = *(const f32x4_t*)(po + (at + s * step) * DP + d);
+      if (s0 + j * NG >= f.y) ml[j] = f32x2_t{-INFINITY, 0.f};
+    }
+    const float mn = fmaxf(fmaxf(fmaxf(ml[0][0], ml[1][0]), fmaxf(ml[2][0], ml[3][0])), M);
+    const float ms = mn == -INFINITY ? 0.f : mn, al = factor<LW>(M, ms);
+    M = mn;
+    L *= al;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] *= al;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float w = factor<LW>(ml[j][0], ms);
+      L += w * ml[j][1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (ml[j][0] != -INFINITY) acc[i] += w * ov[j][i];  // (a part that saw nothing wrote no o)
+    }
   }
+  if constexpr (NG > 1) {
+    *(f32x4_t*)s_o[ng][p] = acc;
+    if (d == 0) {
+      s_ml[ng][p / PR][0] = M;
+      s_ml[ng][p / PR][1] = L;
+    }
+    __syncthreads();
+    if (ng > 0) return;
+#pragma unroll
+    for (int g = 1; g < NG; ++g) M = fmaxf(M, s_ml[g][p / PR][0]);
+    const float ms = M == -INFINITY ? 0.f : M;
+    L = 0.f;
+    acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float w = factor<LW>(s_ml[g][p / PR][0], ms);
+      L += w * s_ml[g][p / PR][1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += w * s_o[g][p][i];
+    }
+  }
+  if (hq >= a.Hq || d >= a.D) return;
   const float inv = L == 0.f ? 0.f : 1.0f / L;
   *(u32x2_t*)(a.out + t * a.o_token + hq * a.o_head + d) =
       u32x2_t{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
-  if (a.lse && d == 0) a.lse[(int64_t)t * a.Hq + hq] = log_sum<LW>(ms, L);
+  if (a.lse && d == 0) a.lse[(int64_t)t * a.Hq + hq] = log_sum<LW>(M == -INFINITY ? 0.f : M, L);
 }
 
 template <class T, int DP, int NQ>
@@ -387,16 +423,31 @@ void decode_dim(const AttendArgs& a, hipStream_t stream) {
     decode_lw<T, 256, NQ>(a, stream);
 }
 
+template <class T, int DP, bool LW>
+void join_rows(const JoinArgs& a, hipStream_t stream) {
+  // Few rows can have many parts each (as many as there are compute units to
+  // share among them): 8 threads share them.  Many rows have few parts, and
+  // most none.
+  constexpr int NG = DP == 256 ? 4 : 8;
+  constexpr int kFewRows = 4096;
+  if ((int64_t)a.T * a.Hq <= kFewRows) {
+    constexpr int rows = kWgThreads / (DP / 4 * NG);
+    join_kernel<T, DP, LW, NG><<<dim3((unsigned)a.T, (unsigned)((a.Hq + rows - 1) / rows)), kWgThreads, 0, stream>>>(a);
+  } else {
+    constexpr int rows = kWgThreads / (DP / 4);
+    join_kernel<T, DP, LW, 1><<<dim3((unsigned)a.T, (unsigned)((a.Hq + rows - 1) / rows)), kWgThreads, 0, stream>>>(a);
+  }
+}
+
 template <class T, bool LW>
 void join_dim(const JoinArgs& a, hipStream_t stream) {
   const int dp = dim_pad(a.D);
-  const dim3 grid((unsigned)a.T, (unsigned)(((int64_t)a.Hq * (dp / 4) + kWgThreads - 1) / kWgThreads));
   if (dp == 64)
-    join_kernel<T, 64, LW><<<grid, kWgThreads, 0, stream>>>(a);
+    join_rows<T, 64, LW>(a, stream);
   else if (dp == 128)
-    join_kernel<T, 128, LW><<<grid, kWgThreads, 0, stream>>>(a);
+    join_rows<T, 128, LW>(a, stream);
   else
-    join_kernel<T, 256, LW><<<grid, kWgThreads, 0, stream>>>(a);
+    join_rows<T, 256, LW>(a, stream);
 }
 
 }  // namespace
