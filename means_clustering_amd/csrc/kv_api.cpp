@@ -1,6 +1,7 @@
 // C ABI of the paged key/value cache: argument checks, and how the attention
 // divides its work.
 #include <algorithm>
+#include <limits>
 #include <string>
 
 #include "../../include/kmeans_cache.h"
@@ -57,18 +58,18 @@ const char* cache_error(const km_kv_cache* c, bool need_v) {
   return nullptr;
 }
 
-// How an attention call is divided into launches and items.
+// How an attention call is divided into launches, and its workspace.
 struct Plan {
   bool decode = false, chunk = false;
-  int bm = 16;                     // decode rows
-  int64_t target[2], parts[2];     // decode, chunk: items wanted per cache head; parts at most
-  int64_t tiles[2];
-  size_t info_at = 0, o_at[2], ml_at[2], bytes = 0;
+  int bm = 16;                // decode rows
+  int64_t pieces = 0;         // decode workgroups
+  int64_t target = 0;         // chunk: items wanted per cache head
+  int64_t tiles = 0;          // ... tiles, at most
+  int64_t parts[2] = {0, 0};  // rows of parts: decode, chunk
+  size_t head_at = 0, info_at = 256, o_at[2] = {0, 0}, ml_at[2] = {0, 0}, bytes = 0;
 };
 
-// Workgroups that the keys are divided into at least, so that 256 compute
-// units stay busy to the end when lengths differ.
-constexpr int64_t kDecodeGroups = 1024, kChunkGroups = 512;
+constexpr int64_t kChunkGroups = 512;  // chunk items in all: two for a compute unit
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -80,17 +81,21 @@ Plan make_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t R, int64_t
   p.bm = rows <= 16 ? 16 : (rows <= 32 ? 32 : 16);
   p.chunk = rows > 32;
   p.decode = !p.chunk || (R > 1 && G <= 16);
-  p.target[0] = std::max<int64_t>(1, kDecodeGroups / Hkv);
-  p.target[1] = std::max<int64_t>(1, kChunkGroups / Hkv);
-  p.tiles[0] = std::min(R, T);
-  p.tiles[1] = std::min(R * ((rows + kChunkRows - 1) / kChunkRows), T * G / kChunkRows + R);
-  const size_t dp = (size_t)dim_pad(D);
-  size_t at = up256((size_t)T * sizeof(int4));
+  const int dp = dim_pad(D);
+  if (p.decode) {
+    p.pieces = (int64_t)kComputeUnits * decode_per_cu(dp, p.bm);
+    p.parts[0] = 2 * p.pieces;
+  }
+  if (p.chunk) {
+    p.target = std::max<int64_t>(1, kChunkGroups / Hkv);
+    p.tiles = std::min(R * ((rows + kChunkRows - 1) / kChunkRows), T * G / kChunkRows + R);
+    p.parts[1] = std::min(2 * p.target, p.target + p.tiles);
+  }
+  size_t at = p.info_at + up256((size_t)T * sizeof(int4));
   for (int i = 0; i < 2; ++i) {
-    p.parts[i] = (i ? p.chunk : p.decode) ? std::min(2 * p.target[i], p.target[i] + p.tiles[i]) : 0;
-    const size_t n = (size_t)p.parts[i] * (size_t)Hkv * (size_t)(i ? kChunkRows : p.bm);
+    const size_t n = (size_t)p.parts[i] * (size_t)(i ? Hkv * kChunkRows : p.bm);
     p.o_at[i] = at;
-    at += up256(n * dp * sizeof(float));
+    at += up256(n * (size_t)dp * sizeof(float));
     p.ml_at[i] = at;
     at += up256(n * sizeof(f32x2_t));
   }
@@ -246,9 +251,8 @@ extern "C" km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, con
                      lw_page >= kMaxStride || lw_head >= kMaxStride))
     return invalid("log_weight must be 16-byte aligned with strides that are multiples of 4");
   const Plan p = make_plan(T, q_heads, cache->heads, cache->dim, R, max_new);
-  for (int i = 0; i < 2; ++i)
-    if ((p.target[i] + p.tiles[i]) * cache->heads > kMaxGroups)
-      return fail(KM_ERR_UNSUPPORTED, "too many requests and heads for one launch");
+  if ((p.target + p.tiles) * cache->heads > kMaxGroups)
+    return fail(KM_ERR_UNSUPPORTED, "too many rows and heads for one launch");
   if (!ws || ws_bytes < p.bytes) return fail(KM_ERR_WORKSPACE, "the workspace is NULL or too small");
   if (!aligned(ws, 256)) return invalid("the workspace must be 256-byte aligned");
   AttendArgs a;
@@ -286,25 +290,36 @@ extern "C" km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, con
   // a window of the whole cache is none
   a.window = window >= width * cache->page_size ? 0 : (int32_t)window;
   a.scale = log_weight ? scale : scale * 1.4426950408889634f;
-  a.info = (int4*)ws;
+  uint8_t* base = (uint8_t*)ws;
+  a.per_head = (int64_t*)(base + p.head_at);
+  a.info = (int4*)(base + p.info_at);
   // most keys that a tile can see, and whether any tile's keys can be divided
   const int64_t room = width * cache->page_size;
   const int64_t keys = std::max<int64_t>(1, a.window ? std::min<int64_t>(room, a.window + max_new + 256) : room);
   bool divided = false;
-  for (int i = 0; i < 2; ++i) {
-    if (!(i ? p.chunk : p.decode)) continue;
-    const int64_t unit = i ? chunk_unit(dim_pad(cache->dim)) : kDecodeUnit;
-    a.lo_rows = i && p.decode ? p.bm : 0;
-    a.hi_rows = i || !p.chunk ? (i ? kMaxI * (int64_t)1024 : p.bm) : p.bm;
-    a.target = (int32_t)p.target[i];
-    a.min_units = i ? 4 : 1;
-    const int64_t most = ((keys + unit - 1) / unit + a.min_units - 1) / a.min_units;
-    a.max_items = (int32_t)std::min(p.target[i] + p.tiles[i], p.tiles[i] * most);
+  if (p.decode) {
+    const int64_t units = (keys + kDecodeUnit - 1) / kDecodeUnit;
+    a.lo_rows = 0;
+    a.hi_rows = p.bm;
+    a.pieces = (int32_t)p.pieces;
+    a.part_o = (float*)(base + p.o_at[0]);
+    a.part_ml = (f32x2_t*)(base + p.ml_at[0]);
+    divided = units > 1;
+    const hipError_t e = launch_decode(a, (int)dt, p.bm, (hipStream_t)stream);
+    if (e != hipSuccess) return launched(e);
+  }
+  if (p.chunk) {
+    const int64_t unit = chunk_unit(dim_pad(cache->dim)), units = (keys + unit - 1) / unit;
+    a.lo_rows = p.decode ? p.bm : 0;
+    a.hi_rows = std::numeric_limits<int64_t>::max();
+    a.target = (int32_t)p.target;
+    a.min_units = 4;
+    const int64_t most = (units + a.min_units - 1) / a.min_units;
+    a.max_items = (int32_t)std::min(p.target + p.tiles, p.tiles * most);
+    a.part_o = (float*)(base + p.o_at[1]);
+    a.part_ml = (f32x2_t*)(base + p.ml_at[1]);
     divided = divided || most > 1;
-    a.part_o = (float*)((uint8_t*)ws + p.o_at[i]);
-    a.part_ml = (f32x2_t*)((uint8_t*)ws + p.ml_at[i]);
-    const hipError_t e = i ? launch_chunk(a, (int)dt, (hipStream_t)stream)
-                           : launch_decode(a, (int)dt, p.bm, (hipStream_t)stream);
+    const hipError_t e = launch_chunk(a, (int)dt, (hipStream_t)stream);
     if (e != hipSuccess) return launched(e);
   }
   if (!divided) return KM_OK;
@@ -314,8 +329,9 @@ extern "C" km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, con
   j.ml0 = (const f32x2_t*)((uint8_t*)ws + p.ml_at[0]);
   j.ml1 = (const f32x2_t*)((uint8_t*)ws + p.ml_at[1]);
   j.bm0 = p.bm;
-  j.parts0 = (int32_t)p.parts[0];
+  j.pieces = (int32_t)p.pieces;
   j.parts1 = (int32_t)p.parts[1];
+  j.per_head = a.per_head;
   j.info = a.info;
   j.out = a.out;
   j.lse = lse;

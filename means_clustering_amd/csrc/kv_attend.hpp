@@ -4,13 +4,18 @@
 // Rows.  The queries of one request that read one cache head are n tokens x G
 // query heads; row m of them is token m / G, head m % G.  A tile is BM rows.
 //
-// Items.  A tile's keys are divided into ranges of `size` units, one item per
-// tile and range.  The size is the same for all requests, so that items cost
-// alike whatever the lengths: all the launch's keys over `target` items, at
-// least min_units.  Lengths are on the device only, so every workgroup works
-// out the division itself, from the lengths of all requests, and takes the
-// item of its own index; there are at most target + (number of tiles) of
-// them, a number that the host knows for its grid.
+// Division.  Lengths are on the device only, so every workgroup works out its
+// share itself, from the lengths of all requests.
+//   Decode launch: all keys of all requests and cache heads, in units of UNIT
+//   keys, form one line, cut into as many equal pieces as there are
+//   workgroups (as many as the GPU holds at once).  So all end together
+//   whatever the lengths, and at most the first and the last request of a
+//   piece are shared with another workgroup.
+//   Chunk launch: a tile's keys are divided into ranges of `size` units, one
+//   item per tile and range.  The size is the same for all requests: all the
+//   launch's keys over `target` items, at least min_units.  A workgroup takes
+//   the item of its own index; there are at most target + (number of tiles)
+//   of them, a number that the host knows for its grid.
 #pragma once
 
 #include "kv_internal.hpp"
@@ -21,6 +26,14 @@ constexpr int kWgThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+
+// First key that the query at slot p and later ones see, rounded down to a
+// whole unit.
+template <int UNIT>
+__device__ __forceinline__ int first_key(const AttendArgs& a, int p) {
+  const int lo = a.window > 0 ? max(p - a.window + 1, 0) : 0;
+  return lo - lo % UNIT;
+}
 
 struct Request {
   int q0, n;   // first query token, query tokens
@@ -42,8 +55,12 @@ __device__ __forceinline__ Request request_of(const AttendArgs& a, int r) {
   q.tiles = rows > a.lo_rows && rows <= a.hi_rows ? (int)((rows + BM - 1) / BM) : 0;
   int64_t keys = q.seq;
   if (a.window > 0) {
-    const int64_t most = (int64_t)a.window + BM / a.G + 2 + UNIT;
-    keys = keys < most ? keys : most;
+    if (q.tiles == 1) {
+      keys -= first_key<UNIT>(a, q.c);
+    } else {
+      const int64_t most = (int64_t)a.window + BM / a.G + 2 + UNIT;
+      keys = keys < most ? keys : most;
+    }
   }
   q.units = (int)((keys + UNIT - 1) / UNIT);
   q.units = max(q.units, 1);
@@ -58,86 +75,210 @@ struct Item {
   __device__ __forceinline__ int part() const { return part0 + tile * splits + split; }
 };
 
-// A request's items, and in the upper 32 bits those of them that are parts.
-__device__ __forceinline__ int64_t items_of(const Request& q, int size) {
-  const int splits = (q.units + size - 1) / size;
-  const int64_t n = (int64_t)q.tiles * splits;
-  return splits > 1 ? n | (n << 32) : n;
+// Inclusive sums over the wavefront (row shifts, then row broadcasts).
+template <int CTRL, int ROWS, class V>
+__device__ __forceinline__ V dpp_(V v) {
+  if constexpr (sizeof(V) == 4) {
+    return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+  } else {
+    const u32x2_t w = __builtin_bit_cast(u32x2_t, v);
+    return __builtin_bit_cast(V, u32x2_t{(unsigned)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROWS, 0xf, false),
+                                         (unsigned)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROWS, 0xf, false)});
+  }
+}
+template <class V>
+__device__ __forceinline__ V wave_scan(V v) {
+  v += dpp_<0x111, 0xf>(v);
+  v += dpp_<0x112, 0xf>(v);
+  v += dpp_<0x114, 0xf>(v);
+  v += dpp_<0x118, 0xf>(v);
+  v += dpp_<0x142, 0xa>(v);
+  v += dpp_<0x143, 0xc>(v);
+  return v;
+}
+
+// A piece of the decode launch's line of keys.  Positions count units; head h
+// of a request that starts at unit u of a head's U is at h * U + u.
+struct Line {
+  int64_t per_head;    // U
+  int64_t from, upto;  // this workgroup's piece
+  int r, off, head;    // request and unit of it at `from`, head
+  Request q;
+};
+// The line of `total` units in n <= total pieces: where piece i starts, and
+// the piece that a position lies in.
+__device__ __forceinline__ int64_t piece_start(int64_t i, int64_t total, int64_t n) { return i * total / n; }
+__device__ __forceinline__ int64_t piece_of(int64_t pos, int64_t total, int64_t n) {
+  return ((pos + 1) * n - 1) / total;
+}
+
+// The piece of workgroup i of n (of as many as there are units, where these
+// are fewer); false where it has none.  Uniform over the workgroup of
+// kWgThreads threads.  scratch: 32 8-byte words of LDS.
+template <int BM, int UNIT>
+__device__ __forceinline__ bool find_piece(const AttendArgs& a, int i, int n, Line& out, int64_t* scratch) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (a.R + kWgThreads - 1) / kWgThreads;
+  const int r0 = tid * per, r1 = min(r0 + per, a.R);
+  Request q0 = {0, 0, 0, 0, 0, 0};
+  if (r0 < r1) q0 = request_of<BM, UNIT>(a, r0);
+  int64_t mine = q0.tiles ? q0.units : 0;
+  for (int r = r0 + 1; r < r1; ++r) {
+    const Request q = request_of<BM, UNIT>(a, r);
+    mine += q.tiles ? q.units : 0;
+  }
+  double sum = wave_scan((double)mine);  // (exact below 2^53)
+  if (lane == 63) scratch[wave] = (int64_t)sum;
+  __syncthreads();
+  int64_t last = (int64_t)sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWgThreads / 64; ++w) {
+    if (w < wave) last += scratch[w];
+    total += scratch[w];
+  }
+  out.per_head = total;
+  const int64_t all = total * a.Hkv, pieces = n < all ? n : all;
+  if (i >= pieces) return false;
+  out.from = piece_start(i, all, pieces);
+  out.upto = piece_start(i + 1, all, pieces);
+  out.head = (int)(out.from / total);
+  const int64_t at = out.from - out.head * total;
+  int64_t first = last - mine;
+  if (at >= first && at < last) {  // this thread's requests hold the position
+    for (int r = r0; r < r1; ++r) {
+      const Request q = r == r0 ? q0 : request_of<BM, UNIT>(a, r);
+      const int u = q.tiles ? q.units : 0;
+      if (at < first + u) {
+        const int v[8] = {r, (int)(at - first), q.q0, q.n, q.seq, q.c, q.tiles, q.units};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) scratch[4 + j] = v[j];
+        break;
+      }
+      first += u;
+    }
+  }
+  __syncthreads();
+  int v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = __builtin_amdgcn_readfirstlane((int)scratch[4 + j]);
+  out.r = v[0];
+  out.off = v[1];
+  out.q = Request{v[2], v[3], v[4], v[5], v[6], v[7]};
+  return true;
+}
+
+// The next request of the launch after request r, the first again after the
+// last (*head moves on).  There is one.  Uniform over the wavefront.
+template <int BM, int UNIT>
+__device__ __forceinline__ Request next_request(const AttendArgs& a, int& r, int& head) {
+  const int lane = threadIdx.x & 63;
+  int base = r + 1;
+  for (;;) {
+    if (base >= a.R) {
+      base = 0;
+      ++head;
+    }
+    Request q = {0, 0, 0, 0, 0, 0};
+    if (base + lane < a.R) q = request_of<BM, UNIT>(a, base + lane);
+    const uint64_t have = __ballot(q.tiles > 0);
+    if (have) {
+      const int l = __builtin_ctzll(have);
+      r = base + l;
+      return Request{__builtin_amdgcn_readlane(q.q0, l), __builtin_amdgcn_readlane(q.n, l),
+                     __builtin_amdgcn_readlane(q.seq, l), __builtin_amdgcn_readlane(q.c, l),
+                     __builtin_amdgcn_readlane(q.tiles, l), __builtin_amdgcn_readlane(q.units, l)};
+    }
+    base += 64;
+  }
 }
 
 // The item of index `it`; false where there is none.  Uniform over the
-// workgroup of kWgThreads threads.  scratch: 16 8-byte words of LDS.
+// workgroup of kWgThreads threads.  scratch: 32 words of LDS.
 template <int BM, int UNIT>
-__device__ __forceinline__ bool find_item(const AttendArgs& a, int it, Item& out, int64_t* scratch) {
+__device__ __forceinline__ bool find_item(const AttendArgs& a, int it, Item& out, int* scratch) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int per = (a.R + kWgThreads - 1) / kWgThreads;
   const int r0 = tid * per, r1 = min(r0 + per, a.R);
   Request q0 = {0, 0, 0, 0, 0, 1};
   if (r0 < r1) q0 = request_of<BM, UNIT>(a, r0);
-  int64_t cost = (int64_t)q0.tiles * q0.units;
+  // (fp32 sums: the size is rounded up by more than they can lose, so the bounds on the numbers of items and parts hold)
+  float cost = (float)q0.tiles * (float)q0.units;
   for (int r = r0 + 1; r < r1; ++r) {
     const Request q = request_of<BM, UNIT>(a, r);
-    cost += (int64_t)q.tiles * q.units;
+    cost += (float)q.tiles * (float)q.units;
   }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) cost += __shfl_xor(cost, d);
-  if (lane == 0) scratch[wave] = cost;
+  cost = wave_scan(cost);
+  float* costs = (float*)scratch;
+  if (lane == 63) costs[wave] = cost;
+  if (tid == 0) scratch[16] = -1;
   __syncthreads();
-  const int64_t total = scratch[0] + scratch[1] + scratch[2] + scratch[3];
-  const int64_t even = (total + a.target - 1) / a.target;
-  const int size = (int)(even > a.min_units ? even : a.min_units);
-  int64_t mine = items_of(q0, size);
-  for (int r = r0 + 1; r < r1; ++r) mine += items_of(request_of<BM, UNIT>(a, r), size);
-  int64_t sum = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t up = __shfl_up(sum, d);
-    if (lane >= d) sum += up;
+  const float total = (costs[0] + costs[1]) + (costs[2] + costs[3]);
+  const int size = max((int)fminf(total * 1.0001f / (float)a.target, 1e9f) + 1, a.min_units);
+  auto count = [&](const Request& q, int& items, int& parts) {
+    const int splits = (q.units + size - 1) / size;
+    items = q.tiles * splits;
+    parts = splits > 1 ? items : 0;
+  };
+  int items, parts;
+  count(q0, items, parts);
+  for (int r = r0 + 1; r < r1; ++r) {
+    int i, p;
+    count(request_of<BM, UNIT>(a, r), i, p);
+    items += i;
+    parts += p;
   }
-  int64_t* waves = scratch + 4;
-  int* found = (int*)(scratch + 8);
-  if (lane == 63) waves[wave] = sum;
-  if (tid == 0) found[0] = -1;
+  int last = wave_scan(items), plast = wave_scan(parts);
+  if (lane == 63) {
+    scratch[4 + wave] = last;
+    scratch[8 + wave] = plast;
+  }
   __syncthreads();
-  for (int w = 0; w < wave; ++w) sum += waves[w];
-  int64_t first = sum - mine;
-  if (it >= (int)first && it < (int)sum) {  // this thread's requests hold the item
+#pragma unroll
+  for (int w = 0; w < kWgThreads / 64 - 1; ++w)
+    if (w < wave) {
+      last += scratch[4 + w];
+      plast += scratch[8 + w];
+    }
+  int first = last - items, pfirst = plast - parts;
+  if (it >= first && it < last) {  // this thread's requests hold the item
     for (int r = r0; r < r1; ++r) {
-      const int64_t n = items_of(r == r0 ? q0 : request_of<BM, UNIT>(a, r), size);
-      if (it < (int)(first + n)) {
-        found[0] = r;
-        found[1] = it - (int)first;
-        found[2] = (int)(first >> 32);
+      const Request q = r == r0 ? q0 : request_of<BM, UNIT>(a, r);
+      int i, p;
+      count(q, i, p);
+      if (it < first + i) {
+        const int v[9] = {r, it - first, pfirst, q.q0, q.n, q.seq, q.c, q.tiles, q.units};
+#pragma unroll
+        for (int j = 0; j < 9; ++j) scratch[16 + j] = v[j];
         break;
       }
-      first += n;
+      first += i;
+      pfirst += p;
     }
   }
   __syncthreads();
-  const int r = __builtin_amdgcn_readfirstlane(found[0]);
-  if (r < 0) return false;
-  out.r = r;
-  out.part0 = __builtin_amdgcn_readfirstlane(found[2]);
-  out.q = request_of<BM, UNIT>(a, r);
+  int v[9];
+#pragma unroll
+  for (int j = 0; j < 9; ++j) v[j] = __builtin_amdgcn_readfirstlane(scratch[16 + j]);
+  if (v[0] < 0) return false;
+  out.r = v[0];
+  out.part0 = v[2];
+  out.q = Request{v[3], v[4], v[5], v[6], v[7], v[8]};
   out.size = size;
   out.splits = (out.q.units + size - 1) / size;
-  const int k = __builtin_amdgcn_readfirstlane(found[1]);
-  out.tile = k / out.splits;
-  out.split = k - out.tile * out.splits;
+  out.tile = v[1] / out.splits;
+  out.split = v[1] - out.tile * out.splits;
   return true;
 }
 
-// The keys that a tile's rows see at all: [lo, hi), lo a multiple of UNIT; and
-// the part of them that is the item's.
-template <int BM, int UNIT>
-__device__ __forceinline__ void key_range(const AttendArgs& a, const Item& w, int& k0, int& k1) {
-  const int i0 = w.tile * BM / a.G, i1 = min((w.tile * BM + BM - 1) / a.G, w.q.n - 1);
-  const int hi = min(w.q.seq, w.q.c + i1 + 1);
-  int lo = a.window > 0 ? max(w.q.c + i0 - a.window + 1, 0) : 0;
-  lo -= lo % UNIT;
-  const int64_t s0 = lo + (int64_t)w.split * w.size * UNIT, s1 = s0 + (int64_t)w.size * UNIT;
-  k0 = (int)(s0 < hi ? s0 : max(hi, 0));
-  k1 = (int)(s1 < hi ? s1 : max(hi, 0));
+// The keys of `size` units from unit `off` of those that rows of tokens
+// i0 .. i1 see at all.
+template <int UNIT>
+__device__ __forceinline__ void key_range(const AttendArgs& a, const Request& q, int i0, int i1, int64_t off,
+                                          int64_t size, int& k0, int& k1) {
+  const int hi = max(min(q.seq, q.c + i1 + 1), 0);
+  const int64_t s0 = first_key<UNIT>(a, q.c + i0) + off * UNIT, s1 = s0 + size * UNIT;
+  k0 = (int)(s0 < hi ? s0 : hi);
+  k1 = (int)(s1 < hi ? s1 : hi);
 }
 
 // A page and whether it is one of the cache's; page 0 stands for those that

@@ -49,7 +49,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
   constexpr int NI = WR * CH / 64;      // ... in this many instructions of 64 pieces
   constexpr int NT = BN / 32, DT = DP / 32;
   constexpr int TP = BN * CH;           // pieces of a tile
-  __shared__ int64_t scratch[16];
+  __shared__ int scratch[32];
   __shared__ __align__(16) u32x4_t s_k[2 * TP];
   __shared__ __align__(16) u32x4_t s_v[2 * TP];
   __shared__ __align__(16) float s_w[2][LW ? BN : 4];
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
   if (head == 0 && w.split == 0)
     for (int i = tok0 + tid; i <= tok1; i += kWgThreads) a.info[w.q.q0 + i] = make_int4(w.part0, w.splits, i, 1);
   int k0, k1;
-  key_range<BM, BN>(a, w, k0, k1);
+  key_range<BN>(a, w.q, tok0, tok1, (int64_t)w.split * w.size, w.size, k0, k1);
   const int32_t* row = a.table + w.r * a.table_stride;
   const int pmask = (1 << a.page_shift) - 1;
 

@@ -40,23 +40,35 @@ struct Tile {
   u32x4_t k[2][DP / 32];
   uint32_t v[8][DP / 32];  // 8 keys x DP / 16 columns
   f32x4_t w[LW ? 2 : 1];
-  int page[2];             // (uniform) the halves' pages
-  bool ok[2];              // ... are in the cache
+  bool ok[2];              // (uniform) the halves' pages are in the cache
 };
+
+// Pages of a step's two halves (uniform): looked up a step before the loads
+// that need them.
+struct Pages {
+  int page[2];
+  bool ok[2];
+};
+__device__ __forceinline__ Pages pages_of(const AttendArgs& a, const int32_t* row, int k) {
+  Pages p;
+  p.page[0] = page_of_uniform(a, row, k, p.ok[0]);
+  p.page[1] = page_of_uniform(a, row, k + 16, p.ok[1]);
+  return p;
+}
 
 template <class T, int DP, int NQ, bool LW>
 struct Decode {
   static constexpr int BM = 16 * NQ, KB = DP / 32, DV = DP / 16, VW = DP / 32;
   static constexpr int LS = DP + 4;  // LDS row of a wavefront's partial result, in floats
 
-  static __device__ __forceinline__ void load(const AttendArgs& a, const int32_t* row, int head, int k, int lane,
+  static __device__ __forceinline__ void load(const AttendArgs& a, const Pages& pg, int head, int k, int lane,
                                               Tile<DP, LW>& t) {
     const int x = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int key = k + 16 * h;
-      t.page[h] = page_of_uniform(a, row, key, t.ok[h]);
-      const int64_t page = t.page[h];
+      t.ok[h] = pg.ok[h];
+      const int64_t page = pg.page[h];
       const int off = key & ((1 << a.page_shift) - 1);
       const uint8_t* kp = a.k + page * a.k_page + off * a.k_slot + head * a.k_head + (x * a.k_slot + g * 16);
 #pragma unroll
@@ -71,7 +83,7 @@ struct Decode {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int key = k + 16 * h;
-      const int64_t page = t.page[h];
+      const int64_t page = pg.page[h];
       const int off = key & ((1 << a.page_shift) - 1);
       const uint8_t* vp = a.v + page * a.v_page + off * a.v_slot + head * a.v_head + (4 * g * a.v_slot + x * (DV * 2));
 #pragma unroll
@@ -97,23 +109,36 @@ struct Decode {
   }
 };
 
-template <class T, int DP, int NQ, bool LW, bool PF>
-__global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void decode_kernel(AttendArgs a) {
+template <class T, int DP, int NQ, bool LW>
+__global__ __launch_bounds__(kWgThreads, decode_per_cu(DP, 16 * NQ)) void decode_kernel(AttendArgs a) {
   using W = Decode<T, DP, NQ, LW>;
   constexpr int BM = W::BM, KB = W::KB, DV = W::DV, LS = W::LS;
-  __shared__ int64_t scratch[16];
+  constexpr bool PF = DP <= 128;  // (two steps' registers)
+  __shared__ int64_t scratch[32];
   __shared__ float s_ml[4][BM][2];
   __shared__ __align__(16) float s_o[4][BM][LS];
-  const int head = blockIdx.x % a.Hkv, it = blockIdx.x / a.Hkv;
-  Item w;
-  if (!find_item<BM, kDecodeUnit>(a, it, w, scratch)) return;
+  Line line;
+  const bool some = find_piece<BM, kDecodeUnit>(a, blockIdx.x, gridDim.x, line, scratch);
   const int tid = threadIdx.x, lane = tid & 63, x = lane & 15, g = lane >> 4;
+  if (blockIdx.x == 0 && tid == 0) *a.per_head = line.per_head;
+  if (!some) return;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int rows = w.q.n * a.G, c = w.q.c;
-  if (head == 0 && w.split == 0)
-    for (int i = tid; i < w.q.n; i += kWgThreads) a.info[w.q.q0 + i] = make_int4(w.part0, w.splits, i, 0);
+  struct {
+    Request q;
+    int r, head, off;
+  } w = {line.q, line.r, line.head, line.off};
+  int64_t pos = line.from;
+  for (;;) {
+  const int64_t left = line.upto - pos;
+  const int len = w.q.units - w.off < left ? w.q.units - w.off : (int)left;
+  const bool whole = len == w.q.units;
+  const int part = 2 * (int)blockIdx.x + (pos == line.from ? 0 : 1);
+  const int rows = w.q.n * a.G, c = w.q.c, head = w.head;
+  if (head == 0 && w.off == 0)
+    for (int i = tid; i < w.q.n; i += kWgThreads)
+      a.info[w.q.q0 + i] = make_int4((int)(uint32_t)pos, w.q.units, i, (int)(pos >> 32) << 1);
   int k0, k1;
-  key_range<BM, kDecodeUnit>(a, w, k0, k1);
+  key_range<kDecodeUnit>(a, w.q, 0, w.q.n - 1, w.off, len, k0, k1);
   const int32_t* row = a.table + w.r * a.table_stride;
 
   // queries: this lane's column of each group of 16 rows
@@ -228,16 +253,20 @@ __global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void de
   };
 
   int k = k0 + 32 * wave;
+  Pages pg = pages_of(a, row, k);
   if constexpr (PF) {
     if (k < k1) {
       Tile<DP, LW> ta, tb;
-      W::load(a, row, head, k, lane, ta);
+      W::load(a, pg, head, k, lane, ta);
+      pg = pages_of(a, row, k + kDecodeUnit);
       for (;;) {
-        if (k + kDecodeUnit < k1) W::load(a, row, head, k + kDecodeUnit, lane, tb);
+        if (k + kDecodeUnit < k1) W::load(a, pg, head, k + kDecodeUnit, lane, tb);
+        pg = pages_of(a, row, k + 2 * kDecodeUnit);
         process(ta, k);
         k += kDecodeUnit;
         if (k >= k1) break;
-        if (k + kDecodeUnit < k1) W::load(a, row, head, k + kDecodeUnit, lane, ta);
+        if (k + kDecodeUnit < k1) W::load(a, pg, head, k + kDecodeUnit, lane, ta);
+        pg = pages_of(a, row, k + 2 * kDecodeUnit);
         process(tb, k);
         k += kDecodeUnit;
         if (k >= k1) break;
@@ -246,7 +275,8 @@ __global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void de
   } else {
     for (; k < k1; k += kDecodeUnit) {
       Tile<DP, LW> t;
-      W::load(a, row, head, k, lane, t);
+      W::load(a, pg, head, k, lane, t);
+      pg = pages_of(a, row, k + kDecodeUnit);
       process(t, k);
     }
   }
@@ -309,7 +339,7 @@ __global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void de
         for (int i = 0; i < 4; ++i) acc[i] += f * ov[i];
       }
     }
-    if (w.splits == 1) {
+    if (whole) {
       const int i = m / a.G, hq = head * a.G + (m - i * a.G);
       const int64_t tok = w.q.q0 + i;
       const float inv = L == 0.f ? 0.f : 1.0f / L;
@@ -318,10 +348,16 @@ __global__ __launch_bounds__(kWgThreads, (DP == 256 || NQ == 2) ? 1 : 2) void de
             u32x2_t{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
       if (a.lse && d == 0) a.lse[tok * a.Hq + hq] = log_sum<LW>(ms, L);
     } else {
-      const int64_t at = ((int64_t)w.part() * a.Hkv + head) * BM + m;
+      const int64_t at = (int64_t)part * BM + m;
       *(f32x4_t*)(a.part_o + at * DP + d) = acc;
       if (d == 0) a.part_ml[at] = f32x2_t{M, L};
     }
+  }
+  pos += len;
+  if (pos >= line.upto) break;
+  w.q = next_request<BM, kDecodeUnit>(a, w.r, w.head);
+  w.off = 0;
+  __syncthreads();  // (s_ml and s_o are read)
   }
 }
 
@@ -335,29 +371,52 @@ __global__ __launch_bounds__(kWgThreads) void join_kernel(JoinArgs a) {
   __shared__ float s_ml[NG > 1 ? NG : 1][NG > 1 ? ROWS : 1][2];
   const int t = blockIdx.x, total = a.query_start[a.R];
   const int4 f = a.info[t];
-  if (t >= total || f.y <= 1) return;
-  const bool chunk = f.w != 0;
-  const int bm = chunk ? kChunkRows : a.bm0, parts = chunk ? a.parts1 : a.parts0;
-  const float* po = chunk ? a.o1 : a.o0;
-  const f32x2_t* pml = chunk ? a.ml1 : a.ml0;
+  if (t >= total) return;
   const int p = threadIdx.x % (PR * ROWS), ng = threadIdx.x / (PR * ROWS);
   const int hq = blockIdx.y * ROWS + p / PR, d = (p % PR) * 4;
   const int head = min(hq, a.Hq - 1) / a.G;
-  const int64_t m = (int64_t)f.z * a.G + (min(hq, a.Hq - 1) - head * a.G);
-  const int64_t tile = m / bm, first = f.x + tile * f.y;
-  if (f.x < 0 || f.z < 0 || first + f.y > parts) return;  // (no such part: more new tokens than max_new)
-  const int64_t at = (first * a.Hkv + head) * bm + (m - tile * bm), step = (int64_t)a.Hkv * bm;
+  const int64_t m = (int64_t)f.z * a.G + (min(hq, a.Hq - 1) - head * a.G);  // row of the request
+  // the parts: n of them, the first at row `at`, the others from row `at1` on every `step` rows
+  const float* po;
+  const f32x2_t* pml;
+  int n;
+  int64_t at, at1, step;
+  if (f.w & 1) {  // chunk launch
+    n = f.y;
+    if (n <= 1) return;
+    const int64_t tile = m / kChunkRows, first = f.x + tile * n;
+    if (f.x < 0 || f.z < 0 || first + n > a.parts1) return;  // (no such part: more new tokens than max_new)
+    po = a.o1;
+    pml = a.ml1;
+    step = (int64_t)a.Hkv * kChunkRows;
+    at = (first * a.Hkv + head) * kChunkRows + (m - tile * kChunkRows);
+    at1 = at + step;
+  } else {  // decode launch: the pieces that the request's units of this head lie in
+    const int64_t per_head = *a.per_head, all = per_head * a.Hkv;
+    const int64_t p0 = head * per_head + (((int64_t)(f.w >> 1) << 32) | (uint32_t)f.x), p1 = p0 + f.y;
+    if (f.y < 1 || m < 0 || m >= a.bm0 || p0 < 0 || p1 > all) return;  // (no such part: more new tokens than max_new)
+    const int64_t pieces = a.pieces < all ? a.pieces : all;
+    const int64_t w0 = piece_of(p0, all, pieces), w1 = piece_of(p1 - 1, all, pieces);
+    n = (int)(w1 - w0) + 1;
+    if (n <= 1) return;
+    po = a.o0;
+    pml = a.ml0;
+    step = 2 * a.bm0;
+    at1 = 2 * (w0 + 1) * a.bm0 + m;  // a piece's first part
+    at = at1 - step + (p0 > piece_start(w0, all, pieces) ? a.bm0 : 0);  // ... its last
+  }
   float M = -INFINITY, L = 0.f;
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s0 = ng; s0 < f.y; s0 += 4 * NG) {
+  for (int s0 = ng; s0 < n; s0 += 4 * NG) {
     f32x2_t ml[4];
     f32x4_t ov[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int s = min(s0 + j * NG, f.y - 1);  // (the last part again, with no weight)
-      ml[j] = pml[at + s * step];
-      ov[j] = *(const f32x4_t*)(po + (at + s * step) * DP + d);
-      if (s0 + j * NG >= f.y) ml[j] = f32x2_t{-INFINITY, 0.f};
+      const int s = min(s0 + j * NG, n - 1);  // (the last part again, with no weight)
+      const int64_t e = s == 0 ? at : at1 + (s - 1) * step;
+      ml[j] = pml[e];
+      ov[j] = *(const f32x4_t*)(po + e * DP + d);
+      if (s0 + j * NG >= n) ml[j] = f32x2_t{-INFINITY, 0.f};
     }
     const float mn = fmaxf(fmaxf(fmaxf(ml[0][0], ml[1][0]), fmaxf(ml[2][0], ml[3][0])), M);
     const float ms = mn == -INFINITY ? 0.f : mn, al = factor<LW>(M, ms);
@@ -404,12 +463,11 @@ __global__ __launch_bounds__(kWgThreads) void join_kernel(JoinArgs a) {
 
 template <class T, int DP, int NQ>
 void decode_lw(const AttendArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)a.max_items * a.Hkv));
-  constexpr bool PF = DP <= 128;
+  const dim3 grid((unsigned)a.pieces);
   if (a.lw)
-    decode_kernel<T, DP, NQ, true, PF><<<grid, kWgThreads, 0, stream>>>(a);
+    decode_kernel<T, DP, NQ, true><<<grid, kWgThreads, 0, stream>>>(a);
   else
-    decode_kernel<T, DP, NQ, false, PF><<<grid, kWgThreads, 0, stream>>>(a);
+    decode_kernel<T, DP, NQ, false><<<grid, kWgThreads, 0, stream>>>(a);
 }
 
 template <class T, int NQ>

@@ -98,15 +98,26 @@ struct AttendArgs {
   // The launch handles the requests with more than lo_rows and at most
   // hi_rows rows (new tokens x G).
   int64_t lo_rows, hi_rows;
-  int32_t target;     // items per cache head that the keys are divided into
-  int32_t min_units;  // least key units of an item
-  int32_t max_items;  // items per cache head, at most
-  float* part_o;      // [parts][Hkv][BM][padded D]
-  f32x2_t* part_ml;   // [parts][Hkv][BM]: m and l
-  int4* info;         // [T]: the request's first part, splits, token in the request, launch (0 decode, 1 chunk)
+  int32_t pieces;     // decode: workgroups
+  int64_t* per_head;  // decode: units of all requests, for one head (written)
+  int32_t target;     // chunk: items per cache head that the keys are divided into
+  int32_t min_units;  // chunk: least key units of an item
+  int32_t max_items;  // chunk: items per cache head, at most
+  // Results of shared rows: o relative to its m, m and l.  Decode: rows
+  // [2 * pieces][BM], two for a workgroup (of its first request, and of its
+  // last if that is another); chunk: rows [parts][Hkv][BM].
+  float* part_o;
+  f32x2_t* part_ml;
+  // [T] for the join.  Decode: (position of the request's first unit, its
+  // units, token in the request, upper half of the position * 2); chunk:
+  // (first part, splits, token in the request, 1).
+  int4* info;
 };
 
 constexpr int kDecodeUnit = 128;  // keys per step of a decode workgroup: 32 for each of its 4 wavefronts
+// Decode workgroups that a compute unit holds (by their registers).
+constexpr int decode_per_cu(int dpad, int bm) { return dpad == 64 ? (bm == 16 ? 3 : 2) : (dpad == 128 && bm == 16 ? 2 : 1); }
+constexpr int kComputeUnits = 256;  // of an MI355X; with fewer the pieces take turns
 constexpr int kChunkRows = 128;   // rows of a chunk workgroup: 32 for each of its 4 wavefronts
 constexpr int chunk_unit(int dpad) { return dpad > 128 ? 32 : 64; }  // keys per step of a chunk workgroup
 inline int dim_pad(int64_t D) { return D <= 64 ? 64 : (D <= 128 ? 128 : 256); }
@@ -118,7 +129,8 @@ hipError_t launch_chunk(const AttendArgs& a, int dt, hipStream_t stream);
 struct JoinArgs {
   const float *o0, *o1;        // parts of the decode and of the chunk launch
   const f32x2_t *ml0, *ml1;
-  int32_t bm0, parts0, parts1;
+  int32_t bm0, pieces, parts1;
+  const int64_t* per_head;
   const int4* info;
   uint16_t* out;
   float* lse;

@@ -469,20 +469,21 @@ def test_attend_past_32_bit_offsets():
         assert bool(((lse.double().cpu() - rl).abs() <= tl).all())
 
 
-def test_attend_same_bits_again_and_on_another_stream():
-    c = Case([(3000, 1), (200, 60), (900, 33)], 8, 2, 128, BF)
-    d = c.device()
-    a, la = kvcache.attend(**d, lse=True)
-    torch.cuda.synchronize()
+@pytest.mark.parametrize("lens", [[(3000, 1), (200, 60), (900, 33)], DECODE, [(129, 1), (700, 1)], [(300, 2)]], ids=len)
+def test_attend_same_bits_again_and_on_another_stream(lens):
+    """With a workspace of any content, on a stream of its own."""
+    c = Case(lens, 8, 2, 128, BF)
+    a, la = c.check()
     ws = kvcache.Workspace(DEV)
     s = torch.cuda.Stream()
+    d = c.device()
+    s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
-        for _ in range(3):
+        for fill in (0, 0xff, 0x7f, 0x3f):
             if ws.buf is not None:
-                ws.buf.fill_(0xff)  # a workspace of any content
+                ws.buf.fill_(fill)
             b, lb = kvcache.attend(**d, lse=True, ws=ws)
-    s.synchronize()
-    assert torch.equal(a, b) and torch.equal(la, lb)
+            assert torch.equal(a, b) and torch.equal(la, lb)
 
 
 def test_step_in_a_graph():
