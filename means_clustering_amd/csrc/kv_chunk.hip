@@ -29,6 +29,12 @@ namespace kmkv {
 namespace {
 
 constexpr int kLoadsDone = 0x0f70;  // s_waitcnt vmcnt(0)
+// Kinds of instructions for the scheduler's groups.
+constexpr int kSchedMfma = 0x008, kSchedLds = 0x100, kSchedValu = 0x402;
+constexpr int kAhead = 6;  // reads of K ahead of the products
+
+// Stands for the values of slots that no row sees: up to 256 elements.
+__device__ const u32x4_t g_zeros[32] = {};
 
 template <class T>
 __device__ __forceinline__ f32x16_t mfma32(const u32x4_t& a, const u32x4_t& b, const f32x16_t& c) {
@@ -52,7 +58,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
   __shared__ int scratch[32];
   __shared__ __align__(16) u32x4_t s_k[2 * TP];
   __shared__ __align__(16) u32x4_t s_v[2 * TP];
-  __shared__ __align__(16) float s_w[2][LW ? BN : 4];
+  __shared__ __align__(16) float s_w[3][LW ? BN : 4];  // weights, a tile ahead of the copies
   __shared__ int s_odd;  // a value was infinite or NaN in a tile that not all rows see, and taken out
   const int head = blockIdx.x % a.Hkv, it = blockIdx.x / a.Hkv;
   Item w;
@@ -117,7 +123,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
     bool ok;
     return page_of_uniform(a, row, kt + wave * WR, ok);
   };
-  auto copy_rows = [&](int kt, int page, int buf, bool whole) __attribute__((always_inline)) {
+  auto copy_rows = [&](int kt, int page, int buf, int wbuf, bool whole) __attribute__((always_inline)) {
     const int off = (kt + wave * WR) & pmask;
     const uint8_t* kp = a.k + page * a.k_page + head * a.k_head + off * a.k_slot;
     const uint8_t* vp = a.v + page * a.v_page + head * a.v_head + off * a.v_slot;
@@ -130,16 +136,18 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
       if (whole || 8 * kc < a.D)
         __builtin_amdgcn_global_load_lds((const void*)(kp + (r * a.k_slot + kc * 16)),
                                          (__attribute__((address_space(3))) void*)(s_k + at), 16, 0, 0);
+      const uint8_t* vr = vp + r * a.v_slot;
+      if (LW && s_w[wbuf][kr] == -INFINITY) vr = (const uint8_t*)g_zeros;
       if (whole || 8 * vc < a.D)
-        __builtin_amdgcn_global_load_lds((const void*)(vp + (r * a.v_slot + vc * 16)),
+        __builtin_amdgcn_global_load_lds((const void*)(vr + vc * 16),
                                          (__attribute__((address_space(3))) void*)(s_v + at), 16, 0, 0);
     }
   };
-  auto copy = [&](int kt, int page, int buf) __attribute__((always_inline)) {
+  auto copy = [&](int kt, int page, int buf, int wbuf) __attribute__((always_inline)) {
     if (a.D == DP)
-      copy_rows(kt, page, buf, true);
+      copy_rows(kt, page, buf, wbuf, true);
     else
-      copy_rows(kt, page, buf, false);
+      copy_rows(kt, page, buf, wbuf, false);
   };
   // Weights of a tile, one for each of the first BN threads.
   auto weight_at = [&](int kt) __attribute__((always_inline)) {
@@ -160,7 +168,6 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
         (void)page_of(a, row, key, ok);
         in = in && ok;
       }
-      if (LW) in = in && s_w[buf][r] != -INFINITY;
       if (!part && in) continue;
       u32x4_t v = s_v[buf * TP + i];
 #pragma unroll
@@ -187,7 +194,8 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
     }
   }
 
-  auto multiply = [&](int kt, int buf) __attribute__((always_inline)) {
+  auto multiply = [&](int kt, int buf, int wbuf) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_setprio(1);
     f32x16_t s[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -196,12 +204,20 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) s[t] = mfma32<T>(s_k[buf * TP + 32 * t * CH + ka[kb]], qf[kb], s[t]);
     }
+    __builtin_amdgcn_sched_group_barrier(kSchedLds, kAhead, 0);
+#pragma unroll
+    for (int i = 0; i < NT * KB - kAhead; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedLds, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(kSchedMfma, kAhead, 0);
+    __builtin_amdgcn_s_setprio(0);
     if (LW) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const f32x4_t wv = *(const f32x4_t*)&s_w[buf][32 * t + 8 * b + 4 * h];
+          const f32x4_t wv = *(const f32x4_t*)&s_w[wbuf][32 * t + 8 * b + 4 * h];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float v = s[t][4 * b + i] * scale + wv[i];
@@ -247,39 +263,63 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
       m_ = mn;
     }
     float sum = 0.f;
+    auto values = [&](int u, u32x4_t(&vf)[DT]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[t][i] = LW ? factor<LW>(s[t][i], ms) : exp2_(fmaf(s[t][i], scale, -ms));
-        sum += s[t][i];
-      }
-    l_ += sum;
-#pragma unroll
-    for (int u = 0; u < 2 * NT; ++u) {
-      u32x4_t pf;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) pf[j] = T::pack(s[u / 2][8 * (u & 1) + 2 * j], s[u / 2][8 * (u & 1) + 2 * j + 1]);
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        u32x4_t vf;
+      for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const char* at = (const char*)s_v + va[d] + (buf * TP + (16 * u + 8 * e) * CH) * 16;
           const u32x2_t two = __builtin_bit_cast(
               u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)at));
-          vf[2 * e] = two[0];
-          vf[2 * e + 1] = two[1];
+          vf[d][2 * e] = two[0];
+          vf[d][2 * e + 1] = two[1];
         }
-        o[d] = mfma32<T>(vf, pf, o[d]);
+    };
+    auto terms = [&](int u, u32x4_t& pf) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = s[u / 2][8 * (u & 1) + j], e = LW ? factor<LW>(v, ms) : exp2_(fmaf(v, scale, -ms));
+        s[u / 2][8 * (u & 1) + j] = e;
+        sum += e;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pf[j] = T::pack(s[u / 2][8 * (u & 1) + 2 * j], s[u / 2][8 * (u & 1) + 2 * j + 1]);
+    };
+    // the values and terms of the next 16 keys are made while these are multiplied
+    u32x4_t vf[2][DT], pf[2];
+    values(0, vf[0]);
+    terms(0, pf[0]);
+#pragma unroll
+    for (int u = 0; u < 2 * NT; ++u) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (u + 1 < 2 * NT) {
+        values(u + 1, vf[(u + 1) & 1]);
+        terms(u + 1, pf[(u + 1) & 1]);
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] = mfma32<T>(vf[u & 1][d], pf[u & 1], o[d]);
+      if (u + 1 < 2 * NT) {
+        __builtin_amdgcn_sched_group_barrier(kSchedLds, 2 * DT, 0);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(kSchedValu, 32 / DT, 0);
+        }
       }
     }
+    l_ += sum;
   };
 
-  int page = 0;
+  int page = 0, wbuf = 0;
   if (k0 < k1) {
-    copy(k0, page_at(k0), 0);
-    if (LW && tid < BN) s_w[0][tid] = weight_at(k0);
+    if (LW) {
+      if (tid < BN) {
+        s_w[0][tid] = weight_at(k0);
+        s_w[1][tid] = weight_at(k0 + BN);
+      }
+      __syncthreads();
+    }
+    copy(k0, page_at(k0), 0, 0);
     page = page_at(k0 + BN);
   }
   __builtin_amdgcn_s_waitcnt(kLoadsDone);
@@ -287,19 +327,22 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
   // One tile: the next is copied to the other buffer meanwhile.
   auto step = [&](int kt, auto b) __attribute__((always_inline)) {
     constexpr int buf = decltype(b)::value;
+    const int wnext = wbuf == 2 ? 0 : wbuf + 1;
     const bool more = kt + BN < k1;
     float wn = 0.f;
     if (more) {
-      copy(kt + BN, page, buf ^ 1);
+      copy(kt + BN, page, buf ^ 1, wnext);
       page = page_at(kt + 2 * BN);
-      if (LW && tid < BN) wn = weight_at(kt + BN);
+      if (LW && tid < BN) wn = weight_at(kt + 2 * BN);
     }
-    if (LW || holes || kt < wfull0 || kt + BN > wfull1) {
-      clean(kt, buf, kt < wfull0 || kt + BN > wfull1);
+    const bool part = kt < wfull0 || kt + BN > wfull1;
+    if (part || holes) {
+      clean(kt, buf, part);
       __syncthreads();
     }
-    if (kt + BN > see0 && kt < see1) multiply(kt, buf);
-    if (LW && more && tid < BN) s_w[buf ^ 1][tid] = wn;
+    if (kt + BN > see0 && kt < see1) multiply(kt, buf, wbuf);
+    if (LW && more && tid < BN) s_w[wnext == 2 ? 0 : wnext + 1][tid] = wn;
+    wbuf = wnext;
     __builtin_amdgcn_s_waitcnt(kLoadsDone);
     __syncthreads();
   };

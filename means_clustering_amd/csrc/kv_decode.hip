@@ -18,7 +18,11 @@
 // depth 8 g + j stands for key 4 g + j of half 0 (j < 4) or key 4 g + j - 4
 // of half 1.  V' has to follow that order: the lane loads DV neighbouring
 // columns of those 8 keys, and a byte permute of two keys' words makes the
-// operands of columns DV x + e.
+// operands of the columns' 16 lanes.
+//
+// The cache is read past the L2 (non-temporal loads): no other workgroup
+// wants a line again, and keeping them costs 5-13% (64 requests of up to
+// 8,192 slots, 8 heads of 128: 175 us with ordinary loads, 164 with these).
 #include "kv_attend.hpp"
 
 namespace kmkv {
@@ -56,10 +60,15 @@ __device__ __forceinline__ Pages pages_of(const AttendArgs& a, const int32_t* ro
   return p;
 }
 
-template <class T, int DP, int NQ, bool LW>
+// WHOLE: rows are DP elements; otherwise the columns from a.D on count as 0.
+template <class T, int DP, int NQ, bool LW, bool WHOLE>
 struct Decode {
   static constexpr int BM = 16 * NQ, KB = DP / 32, DV = DP / 16, VW = DP / 32;
   static constexpr int LS = DP + 4;  // LDS row of a wavefront's partial result, in floats
+  static constexpr int kRun = DV < 8 ? DV : 8;  // neighbouring columns of a lane: one load, so that a load's lanes
+                                                // read whole rows of up to 128 columns
+  // The e-th column that lane x of a group loads.
+  static __device__ __forceinline__ constexpr int column(int x, int e) { return e / kRun * (16 * kRun) + x * kRun + e % kRun; }
 
   static __device__ __forceinline__ void load(const AttendArgs& a, const Pages& pg, int head, int k, int lane,
                                               Tile<DP, LW>& t) {
@@ -73,8 +82,8 @@ struct Decode {
       const uint8_t* kp = a.k + page * a.k_page + off * a.k_slot + head * a.k_head + (x * a.k_slot + g * 16);
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        if (kb * 32 + g * 8 < a.D)
-          t.k[h][kb] = *(const u32x4_t*)(kp + kb * 64);
+        if (WHOLE || kb * 32 + g * 8 < a.D)
+          t.k[h][kb] = __builtin_nontemporal_load((const u32x4_t*)(kp + kb * 64));
         else
           t.k[h][kb] = u32x4_t{0u, 0u, 0u, 0u};
       }
@@ -85,21 +94,21 @@ struct Decode {
       const int key = k + 16 * h;
       const int64_t page = pg.page[h];
       const int off = key & ((1 << a.page_shift) - 1);
-      const uint8_t* vp = a.v + page * a.v_page + off * a.v_slot + head * a.v_head + (4 * g * a.v_slot + x * (DV * 2));
+      const uint8_t* vp = a.v + page * a.v_page + off * a.v_slot + head * a.v_head + (4 * g * a.v_slot + x * (kRun * 2));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t* d = t.v[4 * h + j];
         const uint8_t* s = vp + j * a.v_slot;
         if constexpr (DP == 64) {
           u32x2_t w = {0u, 0u};
-          if (x * DV < a.D) w = *(const u32x2_t*)s;
+          if (WHOLE || column(x, 0) < a.D) w = __builtin_nontemporal_load((const u32x2_t*)s);
           d[0] = w[0];
           d[1] = w[1];
         } else {
 #pragma unroll
           for (int c = 0; c < VW; c += 4) {
             u32x4_t w = {0u, 0u, 0u, 0u};
-            if (x * DV + 2 * c < a.D) w = *(const u32x4_t*)(s + 4 * c);
+            if (WHOLE || column(x, 2 * c) < a.D) w = __builtin_nontemporal_load((const u32x4_t*)(s + column(0, 2 * c) * 2));
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[c + i] = w[i];
           }
@@ -109,9 +118,9 @@ struct Decode {
   }
 };
 
-template <class T, int DP, int NQ, bool LW>
+template <class T, int DP, int NQ, bool LW, bool WHOLE>
 __global__ __launch_bounds__(kWgThreads, decode_per_cu(DP, 16 * NQ)) void decode_kernel(AttendArgs a) {
-  using W = Decode<T, DP, NQ, LW>;
+  using W = Decode<T, DP, NQ, LW, WHOLE>;
   constexpr int BM = W::BM, KB = W::KB, DV = W::DV, LS = W::LS;
   constexpr bool PF = DP <= 128;  // (two steps' registers)
   __shared__ int64_t scratch[32];
@@ -294,7 +303,7 @@ __global__ __launch_bounds__(kWgThreads, decode_per_cu(DP, 16 * NQ)) void decode
       for (int e = 0; e < DV; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int d = DV * (4 * g + i) + e;
+          const int d = W::column(4 * g + i, e);
           const uint32_t v = d < a.D ? vp[d] : 0u;
           if ((v & T::kExp) == T::kExp) {
 #pragma unroll
@@ -317,7 +326,7 @@ __global__ __launch_bounds__(kWgThreads, decode_per_cu(DP, 16 * NQ)) void decode
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < DV; e += 4)
-        *(f32x4_t*)&s_o[wave][16 * q + x][DV * (4 * g + i) + e] =
+        *(f32x4_t*)&s_o[wave][16 * q + x][W::column(4 * g + i, e)] =
             f32x4_t{o[q][e][i], o[q][e + 1][i], o[q][e + 2][i], o[q][e + 3][i]};
   }
   __syncthreads();
@@ -461,13 +470,21 @@ __global__ __launch_bounds__(kWgThreads) void join_kernel(JoinArgs a) {
   if (a.lse && d == 0) a.lse[(int64_t)t * a.Hq + hq] = log_sum<LW>(M == -INFINITY ? 0.f : M, L);
 }
 
+template <class T, int DP, int NQ, bool LW>
+void decode_whole(const AttendArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)a.pieces);
+  if (a.D == DP)
+    decode_kernel<T, DP, NQ, LW, true><<<grid, kWgThreads, 0, stream>>>(a);
+  else
+    decode_kernel<T, DP, NQ, LW, false><<<grid, kWgThreads, 0, stream>>>(a);
+}
+
 template <class T, int DP, int NQ>
 void decode_lw(const AttendArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.pieces);
   if (a.lw)
-    decode_kernel<T, DP, NQ, true><<<grid, kWgThreads, 0, stream>>>(a);
+    decode_whole<T, DP, NQ, true>(a, stream);
   else
-    decode_kernel<T, DP, NQ, false><<<grid, kWgThreads, 0, stream>>>(a);
+    decode_whole<T, DP, NQ, false>(a, stream);
 }
 
 template <class T, int NQ>
