@@ -251,8 +251,8 @@ extern "C" km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, con
                      lw_page >= kMaxStride || lw_head >= kMaxStride))
     return invalid("log_weight must be 16-byte aligned with strides that are multiples of 4");
   const Plan p = make_plan(T, q_heads, cache->heads, cache->dim, R, max_new);
-  if ((p.target + p.tiles) * cache->heads > kMaxGroups)
-    return fail(KM_ERR_UNSUPPORTED, "too many rows and heads for one launch");
+  if (R * cache->heads > kMaxGroups || (p.target + p.tiles) * cache->heads > kMaxGroups)
+    return fail(KM_ERR_UNSUPPORTED, "too many requests, rows and heads for one launch");
   if (!ws || ws_bytes < p.bytes) return fail(KM_ERR_WORKSPACE, "the workspace is NULL or too small");
   if (!aligned(ws, 256)) return invalid("the workspace must be 256-byte aligned");
   AttendArgs a;

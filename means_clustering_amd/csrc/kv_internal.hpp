@@ -43,6 +43,28 @@ struct F16 {
   }
 };
 
+// Inclusive sums over the wavefront (row shifts, then row broadcasts).
+template <int CTRL, int ROWS, class V>
+__device__ __forceinline__ V dpp_(V v) {
+  if constexpr (sizeof(V) == 4) {
+    return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+  } else {
+    const u32x2_t w = __builtin_bit_cast(u32x2_t, v);
+    return __builtin_bit_cast(V, u32x2_t{(unsigned)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROWS, 0xf, false),
+                                         (unsigned)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROWS, 0xf, false)});
+  }
+}
+template <class V>
+__device__ __forceinline__ V wave_scan(V v) {
+  v += dpp_<0x111, 0xf>(v);
+  v += dpp_<0x112, 0xf>(v);
+  v += dpp_<0x114, 0xf>(v);
+  v += dpp_<0x118, 0xf>(v);
+  v += dpp_<0x142, 0xa>(v);
+  v += dpp_<0x143, 0xc>(v);
+  return v;
+}
+
 // ------------------------------------------------------------------ tables ----
 
 struct TablesArgs {

@@ -15,42 +15,17 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ int pages_of(int64_t n, int shift) { return (int)((n + (1ll << shift) - 1) >> shift); }
 
-// Inclusive sum over the workgroup of two values per thread; `tot` gets the
-// totals.  part: 2 * kThreads / 64 ints of LDS.
-__device__ __forceinline__ void block_scan2(int& a, int& b, int& tot_a, int& tot_b, int* part) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int ua = __shfl_up(a, d), ub = __shfl_up(b, d);
-    if (lane >= d) {
-      a += ua;
-      b += ub;
-    }
-  }
-  if (lane == 63) {
-    part[2 * wave] = a;
-    part[2 * wave + 1] = b;
-  }
-  __syncthreads();
-  tot_a = tot_b = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) {
-    if (w == wave) {
-      a += tot_a;
-      b += tot_b;
-    }
-    tot_a += part[2 * w];
-    tot_b += part[2 * w + 1];
-  }
-  __syncthreads();
-}
+// LDS arrays have a word free after every 32, so that threads that walk
+// neighbouring stretches of them meet few banks twice.
+__host__ __device__ constexpr int padded(int i) { return i + (i >> 5); }
 
-// start[r] <= x < start[r+1]; x lies in [0, start[R]).
-__device__ __forceinline__ int owner(const int* start, int R, int x) {
-  int lo = 0, hi = R;  // start[lo] <= x, x < start[hi]
+// start(r) <= x < start(r+1); x lies in [0, start(R)).
+template <class F>
+__device__ __forceinline__ int owner(F&& start, int R, int x) {
+  int lo = 0, hi = R;  // start(lo) <= x, x < start(hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (start[mid] <= x)
+    if (start(mid) <= x)
       lo = mid;
     else
       hi = mid;
@@ -58,25 +33,57 @@ __device__ __forceinline__ int owner(const int* start, int R, int x) {
   return lo;
 }
 
-// The two sums of all R requests, in chunks of kThreads requests.
-template <class F>
-__device__ __forceinline__ void scan_requests(const TablesArgs& a, int* part, F&& put) {
+// The two sums of all R requests, CH at a time: the workgroup stages their
+// new tokens and pages in LDS, each thread adds up its neighbours, the
+// workgroup sums the threads, and each thread gives its requests' sums to
+// put(request, query start, page start).  part: 8 ints of LDS; n, np: padded(CH) + 1.
+template <int CH, class F>
+__device__ __forceinline__ void scan_requests(const TablesArgs& a, int* part, int* n, int* np, F&& put) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int base_q = 0, base_p = 0;
-  for (int r0 = 0; r0 < a.R; r0 += kThreads) {
-    const int r = r0 + threadIdx.x;
-    int n = 0, np = 0, c = 0;
-    if (r < a.R) {
-      c = max(a.ctx[r], 0);
-      n = max(a.fresh[r], 0);
-      np = pages_of((int64_t)c + n, a.page_shift) - pages_of(c, a.page_shift);
+  for (int r0 = 0; r0 < a.R; r0 += CH) {
+    const int m = min(CH, a.R - r0);
+#pragma unroll 8
+    for (int i = tid; i < m; i += kThreads) {
+      const int c = max(a.ctx[r0 + i], 0), f = max(a.fresh[r0 + i], 0);
+      n[padded(i)] = f;
+      np[padded(i)] = pages_of((int64_t)c + f, a.page_shift) - pages_of(c, a.page_shift);
     }
-    int q = n, p = np, tq, tp;
-    block_scan2(q, p, tq, tp, part);
-    if (r < a.R) put(r, c, n, base_q + q - n, base_p + p - np);
-    base_q += tq;
-    base_p += tp;
+    __syncthreads();
+    const int per = (m + kThreads - 1) / kThreads, i0 = min(tid * per, m), i1 = min(i0 + per, m);
+    int q = 0, p = 0;
+#pragma unroll 8
+    for (int i = i0; i < i1; ++i) {
+      q += n[padded(i)];
+      p += np[padded(i)];
+    }
+    int last_q = wave_scan(q), last_p = wave_scan(p);
+    if (lane == 63) {
+      part[wave] = last_q;
+      part[4 + wave] = last_p;
+    }
+    __syncthreads();
+    q = base_q + last_q - q;
+    p = base_p + last_p - p;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) {
+      if (w < wave) {
+        q += part[w];
+        p += part[4 + w];
+      }
+      base_q += part[w];
+      base_p += part[4 + w];
+    }
+#pragma unroll 8
+    for (int i = i0; i < i1; ++i) {
+      const int f = n[padded(i)], g = np[padded(i)];
+      put(r0 + i, q, p);
+      q += f;
+      p += g;
+    }
+    __syncthreads();
   }
-  if (threadIdx.x == 0) put(a.R, 0, 0, base_q, base_p);
+  if (tid == 0) put(a.R, base_q, base_p);
 }
 
 // LDS_R > 0: every workgroup makes the sums itself in LDS (R <= LDS_R), so
@@ -84,28 +91,27 @@ __device__ __forceinline__ void scan_requests(const TablesArgs& a, int* part, F&
 // page_start already.
 template <int LDS_R>
 __global__ __launch_bounds__(kThreads) void tables_kernel(TablesArgs a) {
-  __shared__ int part[2 * kThreads / 64];
-  __shared__ int s_q[LDS_R > 0 ? LDS_R + 1 : 1], s_p[LDS_R > 0 ? LDS_R + 1 : 1];
-  const int *qs = a.query_start, *ps = a.page_start;
+  __shared__ int part[8];
+  __shared__ int s_q[LDS_R > 0 ? padded(LDS_R) + 1 : 1], s_p[LDS_R > 0 ? padded(LDS_R) + 1 : 1];
   if constexpr (LDS_R > 0) {
-    scan_requests(a, part, [&](int r, int c, int n, int q, int p) {
-      s_q[r] = q;
-      s_p[r] = p;
-      if ((r / kThreads) % gridDim.x == blockIdx.x) {  // each workgroup writes its share
-        a.query_start[r] = q;
-        a.page_start[r] = p;
-        if (r < a.R) a.seq_lens[r] = c + n;
-      }
+    scan_requests<LDS_R>(a, part, s_q, s_p, [&](int r, int q, int p) {
+      s_q[padded(r)] = q;
+      s_p[padded(r)] = p;
     });
     __syncthreads();
-    qs = s_q;
-    ps = s_p;
+    for (int r = blockIdx.x * kThreads + threadIdx.x; r <= a.R; r += gridDim.x * kThreads) {
+      a.query_start[r] = s_q[padded(r)];
+      a.page_start[r] = s_p[padded(r)];
+      if (r < a.R) a.seq_lens[r] = max(a.ctx[r], 0) + max(a.fresh[r], 0);
+    }
   }
-  const int total = qs[a.R], taken = ps[a.R];
+  auto qs = [&](int r) { return LDS_R > 0 ? s_q[padded(r)] : a.query_start[r]; };
+  auto ps = [&](int r) { return LDS_R > 0 ? s_p[padded(r)] : a.page_start[r]; };
+  const int total = qs(a.R), taken = ps(a.R);
   const int64_t step = (int64_t)gridDim.x * kThreads, first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   for (int64_t e = first; e < taken; e += step) {
     const int r = owner(ps, a.R, (int)e);
-    const int64_t col = pages_of(max(a.ctx[r], 0), a.page_shift) + (e - ps[r]);
+    const int64_t col = pages_of(max(a.ctx[r], 0), a.page_shift) + (e - ps(r));
     if (col < a.width) a.table[r * a.table_stride + col] = e < a.num_free ? a.free_pages[e] : -1;
   }
   for (int64_t t = first; t < a.T; t += step) {
@@ -113,14 +119,14 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(TablesArgs a) {
     if (t < total) {
       const int r = owner(qs, a.R, (int)t);
       const int c = max(a.ctx[r], 0);
-      const int at = c + ((int)t - qs[r]);
+      const int at = c + ((int)t - qs(r));
       const int col = at >> a.page_shift, have = pages_of(c, a.page_shift);
       int page = -1;
       if (col < a.width) {
         if (col < have) {
           page = a.table[r * a.table_stride + col];
         } else {  // (not from the table: another workgroup writes that entry)
-          const int64_t e = (int64_t)ps[r] + (col - have);
+          const int64_t e = (int64_t)ps(r) + (col - have);
           if (e < a.num_free) page = a.free_pages[e];
         }
       }
@@ -133,11 +139,12 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(TablesArgs a) {
 }
 
 __global__ __launch_bounds__(kThreads) void scan_kernel(TablesArgs a) {
-  __shared__ int part[2 * kThreads / 64];
-  scan_requests(a, part, [&](int r, int c, int n, int q, int p) {
+  constexpr int CH = 4096;
+  __shared__ int part[8], n[padded(CH) + 1], np[padded(CH) + 1];
+  scan_requests<CH>(a, part, n, np, [&](int r, int q, int p) {
     a.query_start[r] = q;
     a.page_start[r] = p;
-    if (r < a.R) a.seq_lens[r] = c + n;
+    if (r < a.R) a.seq_lens[r] = max(a.ctx[r], 0) + max(a.fresh[r], 0);
   });
 }
 

@@ -26,7 +26,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import KM_BF16, KM_F16, KM_F32, KMeansError, Workspace, _ws
+from . import KM_BF16, KM_F16, KM_F32, KMeansError, Workspace
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libkm_cache.so")
@@ -35,6 +35,7 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "kmeans_cache.h")
 __all__ = ["KVCache", "Tables", "Workspace", "append", "attend", "tables"]
 
 _DT = {torch.bfloat16: KM_BF16, torch.float16: KM_F16, torch.float32: KM_F32}
+KM_ERR_WORKSPACE = 3
 _lock = threading.Lock()
 _lib = None
 
@@ -100,57 +101,65 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _ints(t, name: str, device, n=None):
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 vector on {device}")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+# The checks run in every call, which for a decode step costs as much host time as the step takes on the GPU: they
+# compare before they format anything.
+
+def _ints(t, name: str, device, n: int):
+    if t.dtype != torch.int32 or t.device != device or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _rows(t, name: str, device, dtype, shape):
-    if t.device != device or t.dtype != dtype or tuple(t.shape) != shape:
+    s = t.stride()
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
-    s = t.stride()
     if s[2] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     return s
 
 
 def _floats(t, name: str, device, shape):
-    if t.device != device or t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != torch.float32 or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on {device}")
     return t.data_ptr()
 
 
 def _cache(k_cache, v_cache):
-    if k_cache.dim() != 4 or not k_cache.is_cuda:
+    shape = k_cache.shape
+    if len(shape) != 4 or not k_cache.is_cuda:
         raise ValueError("k_cache must be a [pages, page_size, heads, dim] device tensor")
     if k_cache.dtype not in _DT:
         raise TypeError(f"the cache must be bfloat16 or float16, got {k_cache.dtype}")
-    p, n, h, d = k_cache.shape
     a = k_cache.stride()
     b, v = (0, 0, 0, 1), None
     if v_cache is not None:
-        if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device:
+        if v_cache.shape != shape or v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device:
             raise ValueError("v_cache must match k_cache")
         b, v = v_cache.stride(), v_cache.data_ptr()
     if a[3] != 1 or b[3] != 1:
         raise ValueError("the last dimension of the caches must be contiguous")
-    return KVCache(k_cache.data_ptr(), v, p, n, h, d, a[0], a[1], a[2], b[0], b[1], b[2])
+    return KVCache(k_cache.data_ptr(), v, *shape, a[0], a[1], a[2], b[0], b[1], b[2])
 
 
 def _table(block_table, device):
-    if block_table.dtype != torch.int32 or block_table.device != device or block_table.dim() != 2 or (
-            block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError(f"block_table must be an int32 matrix on {device} with contiguous rows")
+    if block_table.dtype != torch.int32 or block_table.device != device or block_table.dim() != 2:
+        raise ValueError(f"block_table must be an int32 matrix on {device}")
     R, width = block_table.shape
-    return R, width, max(block_table.stride(0), width)
+    stride, one = block_table.stride()
+    if one != 1 and width > 1:
+        raise ValueError("the rows of block_table must be contiguous")
+    return R, width, stride if stride > width else width
 
 
-def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+def _stream(device) -> int:
+    """The current stream of `device` (without the Stream object that torch.cuda.current_stream makes)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+_default_ws: dict = {}  # one for each device and stream: calls on different streams may overlap
 
 
 def tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -166,7 +175,7 @@ def tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Te
         raise ValueError("ctx_lens must be a device tensor")
     R, width, stride = _table(block_table, dev)
     c, n = _ints(ctx_lens, "ctx_lens", dev, R), _ints(new_lens, "new_lens", dev, R)
-    f = _ints(free_pages, "free_pages", dev)
+    f = _ints(free_pages, "free_pages", dev, free_pages.numel())
     o = None if pos_offset is None else _ints(pos_offset, "pos_offset", dev, R)
     if total < 0:
         raise ValueError("total must not be negative")
@@ -246,7 +255,7 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     if out is None:
         out = torch.empty((T, hq, cache.dim), dtype=dt, device=dev)
     os_ = _rows(out, "out", dev, dt, (T, hq, cache.dim))
-    R, width, stride = _table(block_table, dev)
+    R, width, tstride = _table(block_table, dev)
     starts, lens = _ints(query_start, "query_start", dev, R + 1), _ints(seq_lens, "seq_lens", dev, R)
     lw_page = lw_head = 0
     if log_weight is not None:
@@ -262,11 +271,20 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     l = None if lse is None else _floats(lse, "lse", dev, (T, hq))
     if max_new is None:
         max_new = T
-    L = lib()
-    # (0 for refused arguments: the call below refuses them too and says why)
-    w = _ws(ws, L.kmeans_kv_attend_workspace(cache, T, hq, R, max_new), dev)
-    _check(L.kmeans_kv_attend(cache, _DT[dt], q.data_ptr(), T, hq, qs[0], qs[1], block_table.data_ptr(), R, width,
-                              stride, starts, lens, _ptr(log_weight), lw_page, lw_head,
-                              cache.dim ** -0.5 if scale is None else scale, window, max_new, out.data_ptr(), os_[0],
-                              os_[1], l, w.data_ptr(), w.numel(), _stream(dev)))
+    L, stream = lib(), _stream(dev)
+    if ws is None:
+        ws = _default_ws.get((dev.index, stream))
+        if ws is None:
+            ws = _default_ws.setdefault((dev.index, stream), Workspace(dev))
+    buf = ws.buf if ws.buf is not None and ws.buf.device == dev else None
+    for _ in range(2):
+        status = L.kmeans_kv_attend(cache, _DT[dt], q.data_ptr(), T, hq, qs[0], qs[1], block_table.data_ptr(), R, width,
+                                    tstride, starts, lens, _ptr(log_weight), lw_page, lw_head,
+                                    cache.dim ** -0.5 if scale is None else scale, window, max_new, out.data_ptr(),
+                                    os_[0], os_[1], l, _ptr(buf), 0 if buf is None else buf.numel(), stream)
+        if status != KM_ERR_WORKSPACE:
+            break
+        # the first call, or a larger one than before (the workspace is the last argument to be refused)
+        buf = ws.get(L.kmeans_kv_attend_workspace(cache, T, hq, R, max_new), dev)
+    _check(status)
     return out if lse is None else (out, lse)
