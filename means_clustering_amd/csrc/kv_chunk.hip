@@ -19,8 +19,9 @@
 // column), so values are stored as they are in memory.
 //
 // LDS rows are DP elements; their 16-byte pieces are permuted by an exclusive
-// or with the row, so that the reads of K (8 rows, one piece column) and of V
-// (4 rows, 2 neighbouring pieces) meet no bank twice.
+// or with a number that goes with the row, so that the lanes served in one
+// cycle (256 bytes: 16 lanes' reads of K, one piece of 16 rows; 32 lanes'
+// reads of V, 4 neighbouring pieces of 4 rows) meet no bank twice.
 #include <type_traits>
 
 #include "kv_attend.hpp"
@@ -35,6 +36,15 @@ constexpr int kAhead = 6;  // reads of K ahead of the products
 
 // Stands for the values of slots that no row sees: up to 256 elements.
 __device__ const u32x4_t g_zeros[32] = {};
+
+template <int CH>
+__device__ __forceinline__ constexpr int k_turn(int row) {
+  return CH == 8 ? (row >> 1) & 7 : row & 15;  // (of 8 pieces two rows lie side by side in the banks)
+}
+template <int CH>
+__device__ __forceinline__ constexpr int v_turn(int row) {
+  return CH == 8 ? (row & 2) * 2 : (row & 3) * 4;
+}
 
 template <class T>
 __device__ __forceinline__ f32x16_t mfma32(const u32x4_t& a, const u32x4_t& b, const f32x16_t& c) {
@@ -132,7 +142,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
       const int r = i * (64 / CH) + lane / CH, pc = lane % CH;  // row of the wavefront's, piece of the LDS row
       const int at = buf * TP + (wave * NI + i) * 64;
       const int kr = wave * WR + r;
-      const int kc = pc ^ (kr & 7), vc = pc ^ ((2 * kr) & (CH - 1) & 14);
+      const int kc = pc ^ k_turn<CH>(kr), vc = pc ^ v_turn<CH>(kr);
       if (whole || 8 * kc < a.D)
         __builtin_amdgcn_global_load_lds((const void*)(kp + (r * a.k_slot + kc * 16)),
                                          (__attribute__((address_space(3))) void*)(s_k + at), 16, 0, 0);
@@ -184,13 +194,13 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
   // LDS addresses of this lane's operands: K's piece 2 kb + h of row x, V's 4 rows of 16 columns for each 32 columns
   int ka[KB], va[DT];
 #pragma unroll
-  for (int kb = 0; kb < KB; ++kb) ka[kb] = x * CH + ((2 * kb + h) ^ (x & 7));
+  for (int kb = 0; kb < KB; ++kb) ka[kb] = x * CH + ((2 * kb + h) ^ k_turn<CH>(x));
   {
     const int r = 4 * h + ((lane & 15) >> 2);
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
       const int col = 32 * d + ((lane >> 4) & 1) * 16 + 4 * (lane & 3);  // elements
-      va[d] = (r * CH + ((col >> 3) ^ ((2 * r) & (CH - 1) & 14))) * 16 + (col & 4) * 2;
+      va[d] = (r * CH + ((col >> 3) ^ v_turn<CH>(r))) * 16 + (col & 4) * 2;
     }
   }
 
