@@ -71,7 +71,8 @@ class Server:
         kvcache.append(None, centroids.transpose(0, 1).to(keys.dtype).contiguous(),
                        means.view(h, clusters, d).transpose(0, 1).to(keys.dtype).contiguous(), self.k, self.v,
                        kept[(at // p).long()] * p + at % p)
-        self.log_weight[kept.long()] = counts.view(h, clusters // p, p).transpose(0, 1).float().log()  # (-inf: empty)
+        # (-inf where a cluster is empty)
+        self.log_weight[kept.long()] = counts.view(h, clusters // p, p).transpose(0, 1).float().log()
         self.free = torch.cat([old[clusters // p:], self.free])
         self.table = torch.cat([kept, self.table[0, slots // p:], old.new_full(((slots - clusters) // p,), -1)])[None]
         self.held = self.held - (slots - clusters)

@@ -141,9 +141,9 @@ size_t kmeans_kv_attend_workspace(const km_kv_cache* cache, int64_t T, int64_t q
  * NaN too).  Rows of tokens outside every request are not written.  Scores,
  * softmax and sums are fp32; the softmax terms are rounded to dt for the
  * product with the values.  Results do not depend on scheduling.
- * Limits: q_heads a multiple of heads; T, R < 2^24, T * q_heads < 2^31, and
- * (R + T * q_heads / heads / 128) * heads below 2^24 or so (beyond:
- * KM_ERR_UNSUPPORTED).
+ * Limits: q_heads a multiple of heads; T, R < 2^24; T * q_heads < 2^31; width *
+ * page_size <= 2^30; (R + T * q_heads / heads / 128) * heads below about 2^24
+ * (beyond: KM_ERR_UNSUPPORTED).
  */
 km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, const void* q, int64_t T, int64_t q_heads,
                            int64_t q_token, int64_t q_head, const int32_t* block_table, int64_t R, int64_t width,

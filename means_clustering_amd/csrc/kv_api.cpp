@@ -27,6 +27,7 @@ km_status launched(hipError_t e) noexcept {
 
 bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
 constexpr int64_t kMaxI = ((int64_t)1 << 31) - 1, kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxRoom = (int64_t)1 << 30;  // slots of a row of the block table
 // A launch has fewer than 2^32 threads: 16 for a row of the append, 256 for
 // an item or a token of the attention.
 constexpr int64_t kMaxRows = (int64_t)1 << 28, kMaxGroups = ((int64_t)1 << 24) - 1;
@@ -50,7 +51,8 @@ const char* cache_error(const km_kv_cache* c, bool need_v) {
   if (c->heads < 1 || c->heads > (1 << 16)) return "cache heads must be 1 to 65536";
   if (c->dim < 16 || c->dim > 256 || c->dim % 16) return "cache dim must be a multiple of 16 up to 256";
   if (!page_size_ok(c->page_size)) return "page_size must be a power of two from 16 to 2^20";
-  if (c->pages < 1 || c->pages > kMaxI / c->page_size) return "pages must be at least 1 and pages * page_size below 2^31";
+  if (c->pages < 1 || c->pages > kMaxI / c->page_size)
+    return "pages must be at least 1 and pages * page_size below 2^31";
   if (!rows_ok(c->k, c->k_page, c->k_slot) || !rows_ok(c->k, c->k_head, 0))
     return "cache keys must be 16-byte aligned with strides that are multiples of 8";
   if (need_v && (!rows_ok(c->v, c->v_page, c->v_slot) || !rows_ok(c->v, c->v_head, 0)))
@@ -179,7 +181,8 @@ extern "C" km_status kmeans_kv_append(const km_kv_cache* cache, km_dtype dt, int
   if (q_heads > 0 && (!rows_ok(q, q_token, q_head) || !rows_ok(q_out, o_token, o_head)))
     return invalid("q and q_out must be 16-byte aligned with strides that are multiples of 8");
   if (!rows_ok(k, k_token, k_head)) return invalid("k must be 16-byte aligned with strides that are multiples of 8");
-  if (v && !rows_ok(v, v_token, v_head)) return invalid("v must be 16-byte aligned with strides that are multiples of 8");
+  if (v && !rows_ok(v, v_token, v_head))
+    return invalid("v must be 16-byte aligned with strides that are multiples of 8");
   if (q_heads > 0 && q == q_out && (q_token != o_token || q_head != o_head))
     return invalid("q_out may be q itself only with the same strides");
   AppendArgs a;
@@ -238,8 +241,8 @@ extern "C" km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, con
   if (dt != KM_BF16 && dt != KM_F16) return invalid("dtype must be KM_BF16 or KM_F16");
   if (window < 0 || window > kMaxI) return invalid("window must be 0 (none) to 2^31 - 1");
   if (!(scale - scale == 0.f)) return invalid("scale must be finite");
-  if (width < 0 || width > kMaxI / cache->page_size || table_stride < width || table_stride >= kMaxStride)
-    return invalid("width must be at least 0, width * page_size below 2^31 and table_stride at least width");
+  if (width < 0 || width > kMaxRoom / cache->page_size || table_stride < width || table_stride >= kMaxStride)
+    return invalid("width must be at least 0, width * page_size at most 2^30 and table_stride at least width");
   if (T == 0 || R == 0 || max_new == 0) return KM_OK;
   if (!rows_ok(q, q_token, q_head) || !rows_ok(out, o_token, o_head))
     return invalid("q and out must be 16-byte aligned with strides that are multiples of 8");
@@ -316,6 +319,7 @@ extern "C" km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, con
     a.min_units = 4;
     const int64_t most = (units + a.min_units - 1) / a.min_units;
     a.max_items = (int32_t)std::min(p.target + p.tiles, p.tiles * most);
+    a.parts = (int32_t)p.parts[1];
     a.part_o = (float*)(base + p.o_at[1]);
     a.part_ml = (f32x2_t*)(base + p.ml_at[1]);
     divided = divided || most > 1;

@@ -47,9 +47,9 @@ __device__ __forceinline__ Request request_of(const AttendArgs& a, int r) {
   Request q;
   q.q0 = clampi(a.query_start[r], 0, a.T);
   q.n = clampi(a.query_start[r + 1], q.q0, a.T) - q.q0;
-  const int64_t room = (int64_t)a.width << a.page_shift;
-  const int sl = max(a.seq_lens[r], 0);
-  q.seq = (int64_t)sl > room ? (int)room : sl;
+  // (room is at most 2^30: positions and keys stay far from the ends of 32 bits)
+  const int room = a.width << a.page_shift, sl = clampi(a.seq_lens[r], 0, 1 << 30);
+  q.seq = min(sl, room);
   q.c = sl - q.n;
   const int64_t rows = (int64_t)q.n * a.G;
   q.tiles = rows > a.lo_rows && rows <= a.hi_rows ? (int)((rows + BM - 1) / BM) : 0;
@@ -179,7 +179,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int it, Item& out
   const int r0 = tid * per, r1 = min(r0 + per, a.R);
   Request q0 = {0, 0, 0, 0, 0, 1};
   if (r0 < r1) q0 = request_of<BM, UNIT>(a, r0);
-  // (fp32 sums: the size is rounded up by more than they can lose, so the bounds on the numbers of items and parts hold)
+  // (fp32 sums: the size is rounded up by more than they can lose, so the bounds on items and parts hold)
   float cost = (float)q0.tiles * (float)q0.units;
   for (int r = r0 + 1; r < r1; ++r) {
     const Request q = request_of<BM, UNIT>(a, r);
@@ -263,7 +263,7 @@ __device__ __forceinline__ void key_range(const AttendArgs& a, const Request& q,
 // are not, so that loads from it stay in bounds.
 __device__ __forceinline__ int page_of(const AttendArgs& a, const int32_t* row, int key, bool& ok) {
   const int col = key >> a.page_shift;
-  const int p = col < a.width ? row[col] : -1;
+  const int p = (unsigned)col < (unsigned)a.width ? row[col] : -1;
   ok = p >= 0 && p < a.pages;
   return ok ? p : 0;
 }
@@ -273,7 +273,7 @@ __device__ __forceinline__ int page_of(const AttendArgs& a, const int32_t* row, 
 __device__ __forceinline__ int page_of_uniform(const AttendArgs& a, const int32_t* row, int key, bool& ok) {
   typedef const __attribute__((address_space(4))) int32_t* table_t;
   const int col = __builtin_amdgcn_readfirstlane(key) >> a.page_shift;
-  const int p = col < a.width ? ((table_t)(uintptr_t)row)[col] : -1;
+  const int p = (unsigned)col < (unsigned)a.width ? ((table_t)(uintptr_t)row)[col] : -1;
   ok = p >= 0 && p < a.pages;
   return ok ? p : 0;
 }

@@ -73,6 +73,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
   const int head = blockIdx.x % a.Hkv, it = blockIdx.x / a.Hkv;
   Item w;
   if (!find_item<BM, BN>(a, it, w, scratch)) return;
+  if (w.splits > 1 && w.part() >= a.parts) return;  // (query_start is not ascending: no such part)
   const int tid = threadIdx.x, lane = tid & 63, x = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rows = w.q.n * a.G, c = w.q.c;
@@ -116,9 +117,9 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
 
   // Are all pages of the item's keys in the cache?  (Uniform.)
   bool hole = false;
-  for (int j = (k0 & ~pmask) + (tid << a.page_shift); j < k1; j += kWgThreads << a.page_shift) {
+  for (int j = (k0 >> a.page_shift) + tid; j <= (k1 - 1) >> a.page_shift; j += kWgThreads) {
     bool ok;
-    (void)page_of(a, row, j, ok);
+    (void)page_of(a, row, j << a.page_shift, ok);
     hole |= !ok;
   }
   const bool holes = __syncthreads_or(hole);

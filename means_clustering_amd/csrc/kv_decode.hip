@@ -65,10 +65,12 @@ template <class T, int DP, int NQ, bool LW, bool WHOLE>
 struct Decode {
   static constexpr int BM = 16 * NQ, KB = DP / 32, DV = DP / 16, VW = DP / 32;
   static constexpr int LS = DP + 4;  // LDS row of a wavefront's partial result, in floats
-  static constexpr int kRun = DV < 8 ? DV : 8;  // neighbouring columns of a lane: one load, so that a load's lanes
-                                                // read whole rows of up to 128 columns
+  // Neighbouring columns of a lane: one load, whose 16 lanes read whole rows of up to 128 columns.
+  static constexpr int kRun = DV < 8 ? DV : 8;
   // The e-th column that lane x of a group loads.
-  static __device__ __forceinline__ constexpr int column(int x, int e) { return e / kRun * (16 * kRun) + x * kRun + e % kRun; }
+  static __device__ __forceinline__ constexpr int column(int x, int e) {
+    return e / kRun * (16 * kRun) + x * kRun + e % kRun;
+  }
 
   static __device__ __forceinline__ void load(const AttendArgs& a, const Pages& pg, int head, int k, int lane,
                                               Tile<DP, LW>& t) {
@@ -94,7 +96,8 @@ struct Decode {
       const int key = k + 16 * h;
       const int64_t page = pg.page[h];
       const int off = key & ((1 << a.page_shift) - 1);
-      const uint8_t* vp = a.v + page * a.v_page + off * a.v_slot + head * a.v_head + (4 * g * a.v_slot + x * (kRun * 2));
+      const uint8_t* vp = a.v + page * a.v_page + off * a.v_slot + head * a.v_head +
+                          (4 * g * a.v_slot + x * (kRun * 2));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t* d = t.v[4 * h + j];
@@ -108,7 +111,8 @@ struct Decode {
 #pragma unroll
           for (int c = 0; c < VW; c += 4) {
             u32x4_t w = {0u, 0u, 0u, 0u};
-            if (WHOLE || column(x, 2 * c) < a.D) w = __builtin_nontemporal_load((const u32x4_t*)(s + column(0, 2 * c) * 2));
+            if (WHOLE || column(x, 2 * c) < a.D)
+              w = __builtin_nontemporal_load((const u32x4_t*)(s + column(0, 2 * c) * 2));
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[c + i] = w[i];
           }
@@ -138,235 +142,237 @@ __global__ __launch_bounds__(kWgThreads, decode_per_cu(DP, 16 * NQ)) void decode
   } w = {line.q, line.r, line.head, line.off};
   int64_t pos = line.from;
   for (;;) {
-  const int64_t left = line.upto - pos;
-  const int len = w.q.units - w.off < left ? w.q.units - w.off : (int)left;
-  const bool whole = len == w.q.units;
-  const int part = 2 * (int)blockIdx.x + (pos == line.from ? 0 : 1);
-  const int rows = w.q.n * a.G, c = w.q.c, head = w.head;
-  if (head == 0 && w.off == 0)
-    for (int i = tid; i < w.q.n; i += kWgThreads)
-      a.info[w.q.q0 + i] = make_int4((int)(uint32_t)pos, w.q.units, i, (int)(pos >> 32) << 1);
-  int k0, k1;
-  key_range<kDecodeUnit>(a, w.q, 0, w.q.n - 1, w.off, len, k0, k1);
-  const int32_t* row = a.table + w.r * a.table_stride;
+    const int64_t left = line.upto - pos;
+    const int len = w.q.units - w.off < left ? w.q.units - w.off : (int)left;
+    const bool whole = len == w.q.units;
+    const int part = 2 * (int)blockIdx.x + (pos == line.from ? 0 : 1);
+    const int rows = w.q.n * a.G, c = w.q.c, head = w.head;
+    if (head == 0 && w.off == 0)
+      for (int i = tid; i < w.q.n; i += kWgThreads)
+        a.info[w.q.q0 + i] = make_int4((int)(uint32_t)pos, w.q.units, i, (int)(pos >> 32) << 1);
+    int k0, k1;
+    key_range<kDecodeUnit>(a, w.q, 0, w.q.n - 1, w.off, len, k0, k1);
+    const int32_t* row = a.table + w.r * a.table_stride;
 
-  // queries: this lane's column of each group of 16 rows
-  u32x4_t qf[NQ][KB];
-  int jmin[NQ], jmax[NQ];
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    const int m = min(16 * q + x, rows - 1);
-    const int i = m / a.G, hq = head * a.G + (m - i * a.G);
-    const uint16_t* qp = a.q + (int64_t)(w.q.q0 + i) * a.q_token + hq * a.q_head + g * 8;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      qf[q][kb] = u32x4_t{0u, 0u, 0u, 0u};
-      if (kb * 32 + g * 8 < a.D) qf[q][kb] = *(const u32x4_t*)(qp + kb * 32);
-    }
-    jmax[q] = min(c + i, k1 - 1);
-    jmin[q] = a.window > 0 ? c + i - a.window + 1 : 0;
-  }
-  // a step whose keys all rows see: from `full0`, up to `full1`
-  const int full1 = min(c + 1, k1), full0 = a.window > 0 ? c + w.q.n - a.window : 0;
-
-  f32x4_t o[NQ][DV];
-  float m_[NQ], l_[NQ];
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    m_[q] = -INFINITY;
-    l_[q] = 0.f;
-#pragma unroll
-    for (int e = 0; e < DV; ++e) o[q][e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  }
-
-  bool some_odd = false;
-  auto process = [&](Tile<DP, LW>& t, int k) __attribute__((always_inline)) {
-    const bool all = k >= full0 && k + 32 <= full1 && t.ok[0] && t.ok[1];
-    bool odd = false;
-    if (!all || LW) {
-      // values of keys that no row sees are taken out, whatever they are
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int key = k + (j < 4 ? 0 : 16) + 4 * g + (j & 3);
-        bool in = (j < 4 ? t.ok[0] : t.ok[1]) && key < k1;
-        if (LW) in = in && t.w[j >> 2][j & 3] != -INFINITY;
-#pragma unroll
-        for (int i = 0; i < W::VW; ++i) {
-          if (!in) t.v[j][i] = 0u;
-          if (!all) odd |= odd_pair<T>(t.v[j][i]);
-        }
-      }
-      // rows differ in what they see and a value is infinite or NaN: take it
-      // out of the product and add it in the end to the rows that see it
-      if (__any(odd)) {
-        some_odd = true;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int i = 0; i < W::VW; ++i) t.v[j][i] = even_pair<T>(t.v[j][i]);
-      }
-    }
-    u32x4_t pf[NQ];
+    // queries: this lane's column of each group of 16 rows
+    u32x4_t qf[NQ][KB];
+    int jmin[NQ], jmax[NQ];
 #pragma unroll
     for (int q = 0; q < NQ; ++q) {
-      float s[8];
+      const int m = min(16 * q + x, rows - 1);
+      const int i = m / a.G, hq = head * a.G + (m - i * a.G);
+      const uint16_t* qp = a.q + (int64_t)(w.q.q0 + i) * a.q_token + hq * a.q_head + g * 8;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb) acc = mfma16<T>(t.k[h][kb], qf[q][kb], acc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v = acc[i] * a.scale;
-          if (LW) v = t.w[h][i] == -INFINITY ? -INFINITY : v + t.w[h][i];  // (whatever the key is)
-          s[4 * h + i] = v;
-        }
+      for (int kb = 0; kb < KB; ++kb) {
+        qf[q][kb] = u32x4_t{0u, 0u, 0u, 0u};
+        if (kb * 32 + g * 8 < a.D) qf[q][kb] = *(const u32x4_t*)(qp + kb * 32);
       }
-      if (!all) {
+      jmax[q] = min(c + i, k1 - 1);
+      jmin[q] = a.window > 0 ? c + i - a.window + 1 : 0;
+    }
+    // a step whose keys all rows see: from `full0`, up to `full1`
+    const int full1 = min(c + 1, k1), full0 = a.window > 0 ? c + w.q.n - a.window : 0;
+
+    f32x4_t o[NQ][DV];
+    float m_[NQ], l_[NQ];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      m_[q] = -INFINITY;
+      l_[q] = 0.f;
+#pragma unroll
+      for (int e = 0; e < DV; ++e) o[q][e] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
+    bool some_odd = false;
+    auto process = [&](Tile<DP, LW>& t, int k) __attribute__((always_inline)) {
+      const bool all = k >= full0 && k + 32 <= full1 && t.ok[0] && t.ok[1];
+      bool odd = false;
+      if (!all || LW) {
+        // values of keys that no row sees are taken out, whatever they are
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int key = k + (j < 4 ? 0 : 16) + 4 * g + (j & 3);
-          const bool see = (j < 4 ? t.ok[0] : t.ok[1]) && key >= jmin[q] && key <= jmax[q];
-          s[j] = see ? s[j] : -INFINITY;
-        }
-      }
-      float mx = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
-      mx = max16(max32(mx));
-      const float mn = fmaxf(m_[q], mx);
-      const float ms = mn == -INFINITY ? 0.f : mn;
-      const float al = factor<LW>(m_[q], ms);
-      float sum = 0.f;
+          bool in = (j < 4 ? t.ok[0] : t.ok[1]) && key < k1;
+          if (LW) in = in && t.w[j >> 2][j & 3] != -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[j] = factor<LW>(s[j], ms);
-        sum += s[j];
-      }
-      m_[q] = mn;
-      l_[q] = l_[q] * al + sum;
-#pragma unroll
-      for (int e = 0; e < DV; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[q][e][i] *= al;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) pf[q][j] = T::pack(s[2 * j], s[2 * j + 1]);
-    }
-#pragma unroll
-    for (int e = 0; e < DV; ++e) {
-      u32x4_t vf;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        vf[j] = __builtin_amdgcn_perm(t.v[2 * j + 1][e / 2], t.v[2 * j][e / 2], e & 1 ? 0x07060302u : 0x05040100u);
-#pragma unroll
-      for (int q = 0; q < NQ; ++q) o[q][e] = mfma16<T>(vf, pf[q], o[q][e]);
-    }
-  };
-
-  int k = k0 + 32 * wave;
-  Pages pg = pages_of(a, row, k);
-  if constexpr (PF) {
-    if (k < k1) {
-      Tile<DP, LW> ta, tb;
-      W::load(a, pg, head, k, lane, ta);
-      pg = pages_of(a, row, k + kDecodeUnit);
-      for (;;) {
-        if (k + kDecodeUnit < k1) W::load(a, pg, head, k + kDecodeUnit, lane, tb);
-        pg = pages_of(a, row, k + 2 * kDecodeUnit);
-        process(ta, k);
-        k += kDecodeUnit;
-        if (k >= k1) break;
-        if (k + kDecodeUnit < k1) W::load(a, pg, head, k + kDecodeUnit, lane, ta);
-        pg = pages_of(a, row, k + 2 * kDecodeUnit);
-        process(tb, k);
-        k += kDecodeUnit;
-        if (k >= k1) break;
-      }
-    }
-  } else {
-    for (; k < k1; k += kDecodeUnit) {
-      Tile<DP, LW> t;
-      W::load(a, pg, head, k, lane, t);
-      pg = pages_of(a, row, k + kDecodeUnit);
-      process(t, k);
-    }
-  }
-
-  if (some_odd) {
-#pragma unroll 1
-    for (int key = k0; key < k1; ++key) {
-      const int kt = key - key % 32;
-      if ((kt / 32) % 4 != wave || (kt >= full0 && kt + 32 <= full1)) continue;  // (not this wavefront's, or whole)
-      bool ok;
-      const int page = page_of_uniform(a, row, key, ok), off = key & ((1 << a.page_shift) - 1);
-      if (!ok || (LW && a.lw[page * a.lw_page + head * a.lw_head + off] == -INFINITY)) continue;
-      const uint16_t* vp = (const uint16_t*)(a.v + page * a.v_page + off * a.v_slot + head * a.v_head);
-#pragma unroll
-      for (int e = 0; e < DV; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int d = W::column(4 * g + i, e);
-          const uint32_t v = d < a.D ? vp[d] : 0u;
-          if ((v & T::kExp) == T::kExp) {
-#pragma unroll
-            for (int q = 0; q < NQ; ++q)
-              if (key >= jmin[q] && key <= jmax[q]) o[q][e][i] += T::lo(v);
+          for (int i = 0; i < W::VW; ++i) {
+            if (!in) t.v[j][i] = 0u;
+            if (!all) odd |= odd_pair<T>(t.v[j][i]);
           }
         }
-    }
-  }
+        // rows differ in what they see and a value is infinite or NaN: take it
+        // out of the product and add it in the end to the rows that see it
+        if (__any(odd)) {
+          some_odd = true;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < W::VW; ++i) t.v[j][i] = even_pair<T>(t.v[j][i]);
+        }
+      }
+      u32x4_t pf[NQ];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        float s[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) acc = mfma16<T>(t.k[h][kb], qf[q][kb], acc);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = acc[i] * a.scale;
+            if (LW) v = t.w[h][i] == -INFINITY ? -INFINITY : v + t.w[h][i];  // (whatever the key is)
+            s[4 * h + i] = v;
+          }
+        }
+        if (!all) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int key = k + (j < 4 ? 0 : 16) + 4 * g + (j & 3);
+            const bool see = (j < 4 ? t.ok[0] : t.ok[1]) && key >= jmin[q] && key <= jmax[q];
+            s[j] = see ? s[j] : -INFINITY;
+          }
+        }
+        float mx = fmaxf(fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])), fmaxf(fmaxf(s[4], s[5]), fmaxf(s[6], s[7])));
+        mx = max16(max32(mx));
+        const float mn = fmaxf(m_[q], mx);
+        const float ms = mn == -INFINITY ? 0.f : mn;
+        const float al = factor<LW>(m_[q], ms);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s[j] = factor<LW>(s[j], ms);
+          sum += s[j];
+        }
+        m_[q] = mn;
+        l_[q] = l_[q] * al + sum;
+#pragma unroll
+        for (int e = 0; e < DV; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[q][e][i] *= al;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pf[q][j] = T::pack(s[2 * j], s[2 * j + 1]);
+      }
+#pragma unroll
+      for (int e = 0; e < DV; ++e) {
+        u32x4_t vf;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          vf[j] = __builtin_amdgcn_perm(t.v[2 * j + 1][e / 2], t.v[2 * j][e / 2], e & 1 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) o[q][e] = mfma16<T>(vf, pf[q], o[q][e]);
+      }
+    };
 
-  // Join the four wavefronts.
-#pragma unroll
-  for (int q = 0; q < NQ; ++q) {
-    const float l = sum16(sum32(l_[q]));
-    if (g == 0) {
-      s_ml[wave][16 * q + x][0] = m_[q];
-      s_ml[wave][16 * q + x][1] = l;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < DV; e += 4)
-        *(f32x4_t*)&s_o[wave][16 * q + x][W::column(4 * g + i, e)] =
-            f32x4_t{o[q][e][i], o[q][e + 1][i], o[q][e + 2][i], o[q][e + 3][i]};
-  }
-  __syncthreads();
-  constexpr int PR = DP / 4;  // 16-byte pieces of a row
-  for (int p = tid; p < BM * PR; p += kWgThreads) {
-    const int m = p / PR, d = (p - m * PR) * 4;
-    if (m >= rows) break;
-    float M = fmaxf(fmaxf(s_ml[0][m][0], s_ml[1][m][0]), fmaxf(s_ml[2][m][0], s_ml[3][m][0]));
-    const float ms = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const float f = factor<LW>(s_ml[v][m][0], ms);
-      L += f * s_ml[v][m][1];
-      const f32x4_t ov = *(const f32x4_t*)&s_o[v][m][d];
-      if (s_ml[v][m][0] != -INFINITY) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] += f * ov[i];
+    int k = k0 + 32 * wave;
+    Pages pg = pages_of(a, row, k);
+    if constexpr (PF) {
+      if (k < k1) {
+        Tile<DP, LW> ta, tb;
+        W::load(a, pg, head, k, lane, ta);
+        pg = pages_of(a, row, k + kDecodeUnit);
+        for (;;) {
+          if (k + kDecodeUnit < k1) W::load(a, pg, head, k + kDecodeUnit, lane, tb);
+          pg = pages_of(a, row, k + 2 * kDecodeUnit);
+          process(ta, k);
+          k += kDecodeUnit;
+          if (k >= k1) break;
+          if (k + kDecodeUnit < k1) W::load(a, pg, head, k + kDecodeUnit, lane, ta);
+          pg = pages_of(a, row, k + 2 * kDecodeUnit);
+          process(tb, k);
+          k += kDecodeUnit;
+          if (k >= k1) break;
+        }
+      }
+    } else {
+      for (; k < k1; k += kDecodeUnit) {
+        Tile<DP, LW> t;
+        W::load(a, pg, head, k, lane, t);
+        pg = pages_of(a, row, k + kDecodeUnit);
+        process(t, k);
       }
     }
-    if (whole) {
-      const int i = m / a.G, hq = head * a.G + (m - i * a.G);
-      const int64_t tok = w.q.q0 + i;
-      const float inv = L == 0.f ? 0.f : 1.0f / L;
-      if (d < a.D)
-        *(u32x2_t*)(a.out + tok * a.o_token + hq * a.o_head + d) =
-            u32x2_t{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
-      if (a.lse && d == 0) a.lse[tok * a.Hq + hq] = log_sum<LW>(ms, L);
-    } else {
-      const int64_t at = (int64_t)part * BM + m;
-      *(f32x4_t*)(a.part_o + at * DP + d) = acc;
-      if (d == 0) a.part_ml[at] = f32x2_t{M, L};
+
+    if (some_odd) {
+#pragma unroll 1
+      for (int key = k0; key < k1; ++key) {
+        const int kt = key - key % 32;
+        if ((kt / 32) % 4 != wave) continue;  // (another wavefront's)
+        const Pages held = pages_of(a, row, kt);
+        if (kt >= full0 && kt + 32 <= full1 && held.ok[0] && held.ok[1]) continue;  // (nothing was taken out)
+        bool ok;
+        const int page = page_of_uniform(a, row, key, ok), off = key & ((1 << a.page_shift) - 1);
+        if (!ok || (LW && a.lw[page * a.lw_page + head * a.lw_head + off] == -INFINITY)) continue;
+        const uint16_t* vp = (const uint16_t*)(a.v + page * a.v_page + off * a.v_slot + head * a.v_head);
+#pragma unroll
+        for (int e = 0; e < DV; ++e)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int d = W::column(4 * g + i, e);
+            const uint32_t v = d < a.D ? vp[d] : 0u;
+            if ((v & T::kExp) == T::kExp) {
+#pragma unroll
+              for (int q = 0; q < NQ; ++q)
+                if (key >= jmin[q] && key <= jmax[q]) o[q][e][i] += T::lo(v);
+            }
+          }
+      }
     }
-  }
-  pos += len;
-  if (pos >= line.upto) break;
-  w.q = next_request<BM, kDecodeUnit>(a, w.r, w.head);
-  w.off = 0;
-  __syncthreads();  // (s_ml and s_o are read)
+
+    // Join the four wavefronts.
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const float l = sum16(sum32(l_[q]));
+      if (g == 0) {
+        s_ml[wave][16 * q + x][0] = m_[q];
+        s_ml[wave][16 * q + x][1] = l;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < DV; e += 4)
+          *(f32x4_t*)&s_o[wave][16 * q + x][W::column(4 * g + i, e)] =
+              f32x4_t{o[q][e][i], o[q][e + 1][i], o[q][e + 2][i], o[q][e + 3][i]};
+    }
+    __syncthreads();
+    constexpr int PR = DP / 4;  // 16-byte pieces of a row
+    for (int p = tid; p < BM * PR; p += kWgThreads) {
+      const int m = p / PR, d = (p - m * PR) * 4;
+      if (m >= rows) break;
+      float M = fmaxf(fmaxf(s_ml[0][m][0], s_ml[1][m][0]), fmaxf(s_ml[2][m][0], s_ml[3][m][0]));
+      const float ms = M == -INFINITY ? 0.f : M;
+      float L = 0.f;
+      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float f = factor<LW>(s_ml[v][m][0], ms);
+        L += f * s_ml[v][m][1];
+        const f32x4_t ov = *(const f32x4_t*)&s_o[v][m][d];
+        if (s_ml[v][m][0] != -INFINITY) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] += f * ov[i];
+        }
+      }
+      if (whole) {
+        const int i = m / a.G, hq = head * a.G + (m - i * a.G);
+        const int64_t tok = w.q.q0 + i;
+        const float inv = L == 0.f ? 0.f : 1.0f / L;
+        if (d < a.D)
+          *(u32x2_t*)(a.out + tok * a.o_token + hq * a.o_head + d) =
+              u32x2_t{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
+        if (a.lse && d == 0) a.lse[tok * a.Hq + hq] = log_sum<LW>(ms, L);
+      } else {
+        const int64_t at = (int64_t)part * BM + m;
+        *(f32x4_t*)(a.part_o + at * DP + d) = acc;
+        if (d == 0) a.part_ml[at] = f32x2_t{M, L};
+      }
+    }
+    pos += len;
+    if (pos >= line.upto) break;
+    w.q = next_request<BM, kDecodeUnit>(a, w.r, w.head);
+    w.off = 0;
+    __syncthreads();  // (s_ml and s_o are read)
   }
 }
 

@@ -125,6 +125,7 @@ struct AttendArgs {
   int32_t target;     // chunk: items per cache head that the keys are divided into
   int32_t min_units;  // chunk: least key units of an item
   int32_t max_items;  // chunk: items per cache head, at most
+  int32_t parts;      // chunk: parts that the workspace holds
   // Results of shared rows: o relative to its m, m and l.  Decode: rows
   // [2 * pieces][BM], two for a workgroup (of its first request, and of its
   // last if that is another); chunk: rows [parts][Hkv][BM].
@@ -138,7 +139,9 @@ struct AttendArgs {
 
 constexpr int kDecodeUnit = 128;  // keys per step of a decode workgroup: 32 for each of its 4 wavefronts
 // Decode workgroups that a compute unit holds (by their registers).
-constexpr int decode_per_cu(int dpad, int bm) { return dpad == 64 ? (bm == 16 ? 3 : 2) : (dpad == 128 && bm == 16 ? 2 : 1); }
+constexpr int decode_per_cu(int dpad, int bm) {
+  return dpad == 64 ? (bm == 16 ? 3 : 2) : (dpad == 128 && bm == 16 ? 2 : 1);
+}
 constexpr int kComputeUnits = 256;  // of an MI355X; with fewer the pieces take turns
 constexpr int kChunkRows = 128;   // rows of a chunk workgroup: 32 for each of its 4 wavefronts
 constexpr int chunk_unit(int dpad) { return dpad > 128 ? 32 : 64; }  // keys per step of a chunk workgroup

@@ -70,7 +70,8 @@ def lib():
             i64, vp, c_int, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
             cache, f = ctypes.POINTER(KVCache), ctypes.c_float
             sig = {
-                "kmeans_kv_tables": (c_int, [vp, vp, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp, vp]),
+                "kmeans_kv_tables": (c_int, [vp, vp, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp,
+                                             vp]),
                 "kmeans_kv_append": (c_int, [cache, c_int, i64, vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, f,
                                              vp, vp, i64, i64, c_int, vp, vp, i64, i64, vp]),
                 "kmeans_kv_attend_workspace": (sz, [cache, i64, i64, i64, i64]),

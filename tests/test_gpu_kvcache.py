@@ -262,8 +262,9 @@ class Case:
     def reference(self):
         """(out, lse, tolerance of out, tolerance of lse) in 64 bits."""
         T, G = self.q.shape[0], self.hq // self.hkv
-        out, tol = torch.zeros(T, self.hq, self.D, dtype=torch.float64), torch.zeros(T, self.hq, self.D, dtype=torch.float64)
-        lse, ltol = torch.full((T, self.hq), -math.inf, dtype=torch.float64), torch.zeros(T, self.hq, dtype=torch.float64)
+        out, tol = (torch.zeros(T, self.hq, self.D, dtype=torch.float64) for _ in range(2))
+        ltol = torch.zeros(T, self.hq, dtype=torch.float64)
+        lse = torch.full_like(ltol, -math.inf)
         t0, u = 0, U[self.dt]
         for r, (s, n) in enumerate(self.lens):
             j = torch.arange(s)
@@ -272,7 +273,9 @@ class Case:
             page = torch.where(held, page, 0)
             for h in range(self.hkv):
                 k, v = self.k[page, j % self.p, h].double(), self.v[page, j % self.p, h].double()
-                lw = self.lw[page, h, j % self.p].double() if self.lw is not None else torch.zeros(s, dtype=torch.float64)
+                lw = torch.zeros(s, dtype=torch.float64)
+                if self.lw is not None:
+                    lw = self.lw[page, h, j % self.p].double()
                 for i in range(n):
                     pos = s - n + i
                     see = held & (j <= pos) & (lw > -math.inf)
@@ -291,7 +294,8 @@ class Case:
                     row = (2.1 * u + 4 * es + (count / 32 + 64) * E)[:, None]
                     o = slice(h * G, (h + 1) * G)
                     out[t0 + i, o], lse[t0 + i, o] = pr @ vv, l
-                    tol[t0 + i, o] = row * (pr @ vv.abs()) + (count * 2.0 ** -25 * vv.abs().max() if self.dt == FP else 0) + 1e-30
+                    small = count * 2.0 ** -25 * vv.abs().max() if self.dt == FP else 0
+                    tol[t0 + i, o] = row * (pr @ vv.abs()) + small + 1e-30
                     ltol[t0 + i, o] = es + (count / 32 + 64) * E + 4 * E * l.abs()
             t0 += n
         return out, lse, tol, ltol
@@ -428,6 +432,26 @@ def test_attend_pages_outside_the_cache_are_not_seen(n):
     c.table[:, 4:] = -1
     want = kvcache.attend(**c.device())
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("n", [1, 60])
+def test_attend_infinite_value_beside_a_page_outside_the_cache(n):
+    """16 slots that are not held share a tile with an infinite value that every row sees."""
+    c = Case([(200, n)], 4, 2, 64, BF)
+    c.set(0, 50, v=math.inf)
+    c.table[0, 2] = -1
+    out = kvcache.attend(**c.device())
+    assert bool((out == math.inf).all())
+
+
+def test_attend_query_starts_that_do_not_ascend():
+    """Overlapping requests (an error of the caller) stay inside every buffer, and later calls are right."""
+    c = Case([(3000, 40), (2000, 40), (900, 40), (100, 40)], 8, 2, 128, BF)
+    d = c.device()
+    for starts in ([0, 160, 0, 160, 0], [-5, 1000, 7, -7, 160], [160, 0, 160, 0, 160]):
+        kvcache.attend(**dict(d, query_start=torch.tensor(starts, dtype=torch.int32, device=DEV), max_new=160))
+    torch.cuda.synchronize()
+    c.check()
 
 
 def test_attend_rows_outside_requests_and_host_bounds():

@@ -24,18 +24,18 @@ def _cache(**kw):
     return kvcache.KVCache(**d)
 
 
-def _append(L, cache=None, dt=km.KM_BF16, T=4, q=FAKE, hq=4, qs=(256, 64), k=FAKE, ks=(128, 64), v=FAKE, vs=(128, 64),
-            qw=None, kw=None, eps=1e-6, pos=FAKE, rope=FAKE, max_pos=100, rot=64, slots=FAKE, out=FAKE + 256,
+def _append(L, cache=None, dt=km.KM_BF16, T=4, q=FAKE, hq=4, qs=(256, 64), k=FAKE, ks=(128, 64), v=FAKE,
+            vs=(128, 64), qw=None, kw=None, eps=1e-6, pos=FAKE, rope=FAKE, max_pos=100, rot=64, slots=FAKE, out=FAKE + 256,
             os=(256, 64)):
-    return L.kmeans_kv_append(cache or _cache(), dt, T, q, hq, *qs, k, *ks, v, *vs, qw, kw, eps, pos, rope, max_pos, rot,
-                              0, slots, out, *os, None)
+    return L.kmeans_kv_append(cache or _cache(), dt, T, q, hq, *qs, k, *ks, v, *vs, qw, kw, eps, pos, rope, max_pos,
+                              rot, 0, slots, out, *os, None)
 
 
 def _attend(L, cache=None, dt=km.KM_BF16, q=FAKE, T=4, hq=4, qs=(256, 64), table=FAKE, R=2, width=8, stride=8,
             starts=FAKE, lens=FAKE, lw=None, lws=(0, 0), scale=0.1, window=0, max_new=4, out=FAKE, os=(256, 64),
             lse=None, ws=FAKE, nb=1 << 40):
-    return L.kmeans_kv_attend(cache or _cache(), dt, q, T, hq, *qs, table, R, width, stride, starts, lens, lw, *lws, scale,
-                              window, max_new, out, *os, lse, ws, nb, None)
+    return L.kmeans_kv_attend(cache or _cache(), dt, q, T, hq, *qs, table, R, width, stride, starts, lens, lw, *lws,
+                              scale, window, max_new, out, *os, lse, ws, nb, None)
 
 
 def _tables(L, ctx=FAKE, new=FAKE, off=None, R=4, p=16, table=FAKE, width=8, stride=8, free=FAKE, nf=5, T=4, seq=FAKE,
@@ -69,8 +69,8 @@ def test_caches(L, bad):
 
 
 def test_null_cache(L):
-    assert L.kmeans_kv_append(None, 1, 4, FAKE, 4, 256, 64, FAKE, 128, 64, FAKE, 128, 64, None, None, 0.0, None, None, 0, 0,
-                              0, None, FAKE, 256, 64, None) == 1
+    assert L.kmeans_kv_append(None, 1, 4, FAKE, 4, 256, 64, FAKE, 128, 64, FAKE, 128, 64, None, None, 0.0, None, None,
+                              0, 0, 0, None, FAKE, 256, 64, None) == 1
     assert "NULL" in _said(L)
 
 
