@@ -105,26 +105,26 @@ def _ptr(t):
 # The checks run in every call, which for a decode step costs as much host time as the step takes on the GPU: they
 # compare before they format anything.
 
-def _ints(t, name: str, device, n: int):
-    if t.dtype != torch.int32 or t.device != device or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries on {device}, got {t.dtype} "
+def _ints(t, name: str, index: int, n: int):
+    if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 vector of {n} entries on cuda:{index}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(t, name: str, device, dtype, shape):
-    s = t.stride()
-    if t.shape != shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on {device}, got {t.dtype} "
+def _rows(t, name: str, index: int, dtype, shape):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape} on cuda:{index}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
+    s = t.stride()
     if s[2] != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     return s
 
 
-def _floats(t, name: str, device, shape):
-    if t.dtype != torch.float32 or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on {device}")
+def _floats(t, name: str, index: int, shape):
+    if t.dtype is not torch.float32 or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of shape {shape} on cuda:{index}")
     return t.data_ptr()
 
 
@@ -137,7 +137,8 @@ def _cache(k_cache, v_cache):
     a = k_cache.stride()
     b, v = (0, 0, 0, 1), None
     if v_cache is not None:
-        if v_cache.shape != shape or v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device:
+        if v_cache.shape != shape or v_cache.dtype is not k_cache.dtype or (
+                v_cache.get_device() != k_cache.get_device()):
             raise ValueError("v_cache must match k_cache")
         b, v = v_cache.stride(), v_cache.data_ptr()
     if a[3] != 1 or b[3] != 1:
@@ -145,20 +146,18 @@ def _cache(k_cache, v_cache):
     return KVCache(k_cache.data_ptr(), v, *shape, a[0], a[1], a[2], b[0], b[1], b[2])
 
 
-def _table(block_table, device):
-    if block_table.dtype != torch.int32 or block_table.device != device or block_table.dim() != 2:
-        raise ValueError(f"block_table must be an int32 matrix on {device}")
-    R, width = block_table.shape
-    stride, one = block_table.stride()
+def _table(t, index: int):
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.get_device() != index:
+        raise ValueError(f"block_table must be an int32 matrix on cuda:{index}")
+    R, width = t.shape
+    stride, one = t.stride()
     if one != 1 and width > 1:
         raise ValueError("the rows of block_table must be contiguous")
     return R, width, stride if stride > width else width
 
 
-def _stream(device) -> int:
-    """The current stream of `device` (without the Stream object that torch.cuda.current_stream makes)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
+# The handle of a device's current stream (torch.cuda.current_stream would make a Stream object of it).
+_stream = torch._C._cuda_getCurrentRawStream
 
 _default_ws: dict = {}  # one for each device and stream: calls on different streams may overlap
 
@@ -171,8 +170,8 @@ def tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Te
     ``ctx_lens`` are taken from ``free_pages`` in order.  ``total`` is the number of new tokens (the capacity of
     ``positions`` and ``slots``).  ``pos_offset`` is added to positions.
     """
-    dev = ctx_lens.device
-    if dev.type != "cuda":
+    dev = ctx_lens.get_device()
+    if dev < 0:
         raise ValueError("ctx_lens must be a device tensor")
     R, width, stride = _table(block_table, dev)
     c, n = _ints(ctx_lens, "ctx_lens", dev, R), _ints(new_lens, "new_lens", dev, R)
@@ -181,7 +180,7 @@ def tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Te
     if total < 0:
         raise ValueError("total must not be negative")
     # one allocation, five views: seq_lens, query_start, page_start, positions, slots
-    seq, qs, ps, pos, slots = torch.empty(3 * R + 2 + 2 * total, dtype=torch.int32, device=dev).split_with_sizes(
+    seq, qs, ps, pos, slots = ctx_lens.new_empty(3 * R + 2 + 2 * total).split_with_sizes(
         (R, R + 1, R + 1, total, total))
     _check(lib().kmeans_kv_tables(c, n, o, R, page_size, block_table.data_ptr(), width, stride, f,
                                   free_pages.shape[0], total, seq.data_ptr(), qs.data_ptr(), ps.data_ptr(),
@@ -202,7 +201,7 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_ca
     the queries (``out``, or a new tensor; ``out`` may be q).
     """
     cache = _cache(k_cache, v_cache if v is not None else None)
-    dev, dt = k_cache.device, k_cache.dtype
+    dev, dt = k_cache.get_device(), k_cache.dtype
     T, heads, dim = k.shape[0], cache.heads, cache.dim
     ks = _rows(k, "k", dev, dt, (T, heads, dim))
     if v is not None and v_cache is None:
@@ -213,7 +212,7 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_ca
         hq = q.shape[1]
         qs = _rows(q, "q", dev, dt, (T, hq, dim))
         if out is None:
-            out = torch.empty((T, hq, dim), dtype=dt, device=dev)
+            out = k.new_empty((T, hq, dim))
         os_ = _rows(out, "out", dev, dt, (T, hq, dim))
     if (rope is None) != (positions is None):
         raise ValueError("rope and positions go together")
@@ -250,23 +249,23 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     row's sum.  Returns out, or (out, lse).
     """
     cache = _cache(k_cache, v_cache)
-    dev, dt = k_cache.device, k_cache.dtype
+    dev, dt = k_cache.get_device(), k_cache.dtype
     T, hq = q.shape[0], q.shape[1]
     qs = _rows(q, "q", dev, dt, (T, hq, cache.dim))
     if out is None:
-        out = torch.empty((T, hq, cache.dim), dtype=dt, device=dev)
+        out = q.new_empty((T, hq, cache.dim))
     os_ = _rows(out, "out", dev, dt, (T, hq, cache.dim))
     R, width, tstride = _table(block_table, dev)
     starts, lens = _ints(query_start, "query_start", dev, R + 1), _ints(seq_lens, "seq_lens", dev, R)
     lw_page = lw_head = 0
     if log_weight is not None:
-        if log_weight.shape != (cache.pages, cache.heads, cache.page_size) or log_weight.dtype != torch.float32 or \
-                log_weight.device != dev or log_weight.stride(2) != 1:
-            raise ValueError(f"log_weight must be float32 [{cache.pages}, {cache.heads}, {cache.page_size}] on {dev} "
-                             "with contiguous rows")
+        if log_weight.shape != (cache.pages, cache.heads, cache.page_size) or (
+                log_weight.dtype is not torch.float32 or log_weight.get_device() != dev or log_weight.stride(2) != 1):
+            raise ValueError(f"log_weight must be float32 [{cache.pages}, {cache.heads}, {cache.page_size}] on "
+                             f"cuda:{dev} with contiguous rows")
         lw_page, lw_head = log_weight.stride(0), log_weight.stride(1)
     if lse is True:
-        lse = torch.empty((T, hq), dtype=torch.float32, device=dev)
+        lse = q.new_empty((T, hq), dtype=torch.float32)
     elif lse is False:
         lse = None
     l = None if lse is None else _floats(lse, "lse", dev, (T, hq))
@@ -274,10 +273,10 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
         max_new = T
     L, stream = lib(), _stream(dev)
     if ws is None:
-        ws = _default_ws.get((dev.index, stream))
+        ws = _default_ws.get((dev, stream))
         if ws is None:
-            ws = _default_ws.setdefault((dev.index, stream), Workspace(dev))
-    buf = ws.buf if ws.buf is not None and ws.buf.device == dev else None
+            ws = _default_ws.setdefault((dev, stream), Workspace())
+    buf = ws.buf if ws.buf is not None and ws.buf.get_device() == dev else None
     for _ in range(2):
         status = L.kmeans_kv_attend(cache, _DT[dt], q.data_ptr(), T, hq, qs[0], qs[1], block_table.data_ptr(), R, width,
                                     tstride, starts, lens, _ptr(log_weight), lw_page, lw_head,
@@ -286,6 +285,6 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
         if status != KM_ERR_WORKSPACE:
             break
         # the first call, or a larger one than before (the workspace is the last argument to be refused)
-        buf = ws.get(L.kmeans_kv_attend_workspace(cache, T, hq, R, max_new), dev)
+        buf = ws.get(L.kmeans_kv_attend_workspace(cache, T, hq, R, max_new), q.device)
     _check(status)
     return out if lse is None else (out, lse)
