@@ -243,8 +243,9 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int it, Item& out
   out.q = Request{v[3], v[4], v[5], v[6], v[7], v[8]};
   out.size = size;
   out.splits = (out.q.units + size - 1) / size;
-  out.tile = v[1] / out.splits;
-  out.split = v[1] - out.tile * out.splits;
+  const int k = v[1] / out.splits;
+  out.tile = out.q.tiles - 1 - k;  // (last rows first: they see the most keys)
+  out.split = v[1] - k * out.splits;
   return true;
 }
 
