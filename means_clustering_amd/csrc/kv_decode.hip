@@ -20,9 +20,22 @@
 // columns of those 8 keys, and a byte permute of two keys' words makes the
 // operands of the columns' 16 lanes.
 //
-// The cache is read past the L2 (non-temporal loads): no other workgroup
-// wants a line again, and keeping them costs 5-13% (64 requests of up to
-// 8,192 slots, 8 heads of 128: 175 us with ordinary loads, 164 with these).
+// What bounds it, measured (MI355X; a plain read of 1 GB reaches 6.3 TB/s, a
+// copy 4.9): 64 requests of up to 8,191 slots with 8 heads of 128 read 847 MB
+// in 155 us (5.5 TB/s), two of 131,000 slots with weights 428 MB in 84 us
+// (5.1 TB/s), the join after them 5-6 us; a single request of 500 slots takes
+// 8 us, the latencies of its lengths, pages, keys and of the two launches.
+//   * Equal pieces of one line of keys against items of equal size per
+//     request: 255 requests of D = 64 149 us against 180, 63 requests of 5 new
+//     tokens 176 against 195 (items leave the last round of workgroups short).
+//   * Page numbers by scalar loads, a step ahead: 64 requests 175 us against
+//     199 with vector loads, whose wait also waited for keys in flight.
+//   * Values are read past the caches (non-temporal loads; a load's lanes take
+//     whole lines, which nobody wants again): 64 requests 161 us against 176.
+//     Keys are not: a load takes half of each line, so the other half is
+//     wanted at once (both so: 164 us, a third more reads of the L2).
+// P is rounded to the cache's type for the matrix cores: its relative error of
+// 2^-8 (2^-11) is that of the result's own rounding.  m, l and o are fp32.
 #include "kv_attend.hpp"
 
 namespace kmkv {
@@ -85,7 +98,7 @@ struct Decode {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         if (WHOLE || kb * 32 + g * 8 < a.D)
-          t.k[h][kb] = __builtin_nontemporal_load((const u32x4_t*)(kp + kb * 64));
+          t.k[h][kb] = *(const u32x4_t*)(kp + kb * 64);
         else
           t.k[h][kb] = u32x4_t{0u, 0u, 0u, 0u};
       }
@@ -506,11 +519,13 @@ void decode_dim(const AttendArgs& a, hipStream_t stream) {
 
 template <class T, int DP, bool LW>
 void join_rows(const JoinArgs& a, hipStream_t stream) {
-  // Few rows can have many parts each (as many as there are compute units to
-  // share among them): 8 threads share them.  Many rows have few parts, and
-  // most none.
+  // Few rows can have many parts each (as many as there are workgroups to
+  // share among them): 8 threads share them.  Many rows have few parts or
+  // none.  (Measured, whole calls: 56 rows of 146 parts 87 us with 8 threads,
+  // 99 with one; 4,064 rows of 4 parts 143 us with 8, 139 with one; 16,352
+  // rows of one or two 178 against 163.)
   constexpr int NG = DP == 256 ? 4 : 8;
-  constexpr int kFewRows = 4096;
+  constexpr int kFewRows = 1024;
   if ((int64_t)a.T * a.Hq <= kFewRows) {
     constexpr int rows = kWgThreads / (DP / 4 * NG);
     join_kernel<T, DP, LW, NG><<<dim3((unsigned)a.T, (unsigned)((a.Hq + rows - 1) / rows)), kWgThreads, 0, stream>>>(a);

