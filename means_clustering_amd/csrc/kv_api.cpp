@@ -129,7 +129,8 @@ extern "C" km_status kmeans_kv_tables(const int32_t* ctx_lens, const int32_t* ne
                                       int64_t table_stride, const int32_t* free_pages, int64_t num_free, int64_t T,
                                       int32_t* seq_lens, int32_t* query_start, int32_t* page_start,
                                       int32_t* positions, int32_t* slots, void* stream) {
-  if (R < 0 || R >= kMaxI || T < 0 || T > kMaxI) return invalid("R and T must be 0 to 2^31 - 1");
+  if (R < 0 || R > kMaxGroups || T < 0 || T > kMaxI)
+    return invalid("R must be 0 to 2^24 - 1 and T 0 to 2^31 - 1");
   if (!page_size_ok(page_size)) return invalid("page_size must be a power of two from 16 to 2^20");
   if (width < 0 || width > kMaxI / page_size || table_stride < width || table_stride >= kMaxStride)
     return invalid("width must be at least 0, width * page_size below 2^31 and table_stride at least width");

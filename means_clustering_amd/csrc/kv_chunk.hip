@@ -92,7 +92,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
   const int head = blockIdx.x % a.Hkv, it = blockIdx.x / a.Hkv;
   Item w;
   if (!find_item<BM, BN>(a, it, w, scratch)) return;
-  if (w.splits > 1 && w.part() >= a.parts) return;  // (query_start is not ascending: no such part)
+  if (w.splits > 1 && (unsigned)w.part() >= (unsigned)a.parts) return;  // (query_start is not ascending: no such part)
   const int tid = threadIdx.x, lane = tid & 63, x = lane & 31, h = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rows = w.q.n * a.G, c = w.q.c;

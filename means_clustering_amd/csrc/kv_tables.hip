@@ -119,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(TablesArgs a) {
   for (int64_t e = first; e < taken; e += step) {
     const int r = owner(ps, a.R, (int)e);
     const int64_t col = pages_of(max(a.ctx[r], 0), a.page_shift) + (e - ps(r));
-    if (col < a.width) a.table[r * a.table_stride + col] = e < a.num_free ? a.free_pages[e] : -1;
+    if (col >= 0 && col < a.width) a.table[r * a.table_stride + col] = e < a.num_free ? a.free_pages[e] : -1;
   }
   for (int64_t t = first; t < a.T; t += step) {
     int pos = 0, slot = -1;
@@ -129,12 +129,12 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(TablesArgs a) {
       const int at = c + ((int)t - qs(r));
       const int col = at >> a.page_shift, have = pages_of(c, a.page_shift);
       int page = -1;
-      if (col < a.width) {
+      if ((unsigned)col < (unsigned)a.width) {  // (lengths whose sums pass 2^31 stay inside the table too)
         if (col < have) {
           page = a.table[r * a.table_stride + col];
         } else {  // (not from the table: another workgroup writes that entry)
           const int64_t e = (int64_t)ps(r) + (col - have);
-          if (e < a.num_free) page = a.free_pages[e];
+          if (e >= 0 && e < a.num_free) page = a.free_pages[e];
         }
       }
       pos = at + (a.offset ? a.offset[r] : 0);

@@ -98,6 +98,21 @@ def test_tables_edges():
     _check_tables([100], [20000], 400, 64, 400)                         # one long prompt
 
 
+def test_tables_lengths_near_the_end_of_32_bits():
+    """Slots that no table row can hold: nothing is written beside the table, and the tokens get no slot."""
+    top = 2 ** 31 - 1
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    big = torch.full((4, 9), -77, dtype=torch.int32, device=DEV)
+    t = kvcache.tables(i32([top, top - 20, 0]), i32([5, 9, 2]), big[1:, :6], i32([3, 4, 5]), 16, 16)
+    assert t.slots.tolist()[:14] == [-1] * 14
+    assert t.query_start.tolist() == [0, 5, 14, 16]
+    keep = big.clone()
+    keep[3, 0] = -77
+    assert bool((keep == -77).all())
+    kvcache.tables(i32([0, 0, 0]), i32([top, top, top]), big[1:, :6], i32([3, 4, 5]), 16, 16)  # the sum wraps
+    assert bool((big[0] == -77).all()) and bool((big[:, 6:] == -77).all())
+
+
 # ------------------------------------------------------------------------------------------------------ append ----
 
 def _rope(max_pos, rot):
@@ -335,6 +350,22 @@ def test_attend_decode(dt, hq, hkv, D, p, window, weighted, layout):
     (20, 1, 128, 16, 0, False, "slots"), (1, 1, 16, 16, 1, False, "slots"), (2, 2, 208, 32, 0, True, "joint")])
 def test_attend_chunks(dt, hq, hkv, D, p, window, weighted, layout):
     Case(CHUNKS, hq, hkv, D, dt, p, window, weighted, layout).check()
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attend_random_shapes(seed):
+    r = random.Random(seed)
+    hkv, group = r.choice([1, 2, 3]), r.choice([1, 2, 3, 5, 8, 12, 17])
+    most = r.choice([1, 1, 2, 6, 40, 150])
+    lens = []
+    for _ in range(r.choice([1, 2, 5, 9])):
+        s = int(math.exp(r.uniform(0, math.log(900))))
+        lens.append((s, min(r.randint(0, most), s + r.choice([0, 0, 2]))))
+    if not any(n for _, n in lens):
+        lens[0] = (lens[0][0], 1)
+    Case(lens, hkv * group, hkv, 16 * r.randint(1, 16), r.choice([BF, FP]), r.choice([16, 32, 64, 256]),
+         r.choice([0, 0, 1, 17, 100, 5000]), r.random() < 0.4, r.choice(["slots", "heads", "joint"]), seed,
+         sharp=r.choice([0.3, 1.0, 4.0])).check()
 
 
 @pytest.mark.parametrize("n,hq", [(2, 8), (5, 3), (4, 8), (8, 4), (33, 1)])

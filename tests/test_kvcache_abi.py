@@ -114,7 +114,7 @@ def test_attend_limits_and_workspace(L):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(R=-1), dict(T=-1), dict(p=8), dict(p=48), dict(width=-1), dict(stride=7), dict(width=1 << 27, stride=1 << 27),
+    dict(R=-1), dict(R=1 << 24), dict(T=-1), dict(p=8), dict(p=48), dict(width=-1), dict(stride=7), dict(width=1 << 27, stride=1 << 27),
     dict(nf=-1), dict(qs=None), dict(ps=None), dict(ctx=None), dict(new=None), dict(seq=None), dict(table=None),
     dict(free=None), dict(pos=None), dict(slots=None), dict(ctx=ODD2), dict(off=ODD2), dict(slots=ODD2)], ids=str)
 def test_tables_refusals(L, bad):
