@@ -1,6 +1,9 @@
 """The paged key/value cache library on the CPU: it loads, exports every declared symbol, and refuses bad arguments
 before any HIP call, so no GPU is needed."""
-import ctypes
+import glob
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -130,3 +133,34 @@ def test_python_binding_rejects_host_tensors():
         kvcache.attend(c[0, :1], c, c, torch.zeros(1, 2, dtype=torch.int32), i, i)
     with pytest.raises(ValueError, match="device"):
         kvcache.tables(i, i, torch.zeros(1, 2, dtype=torch.int32), i, 16, 1)
+
+
+def test_checks_under_asan_ubsan(tmp_path):
+    """The host side (argument checks, plans, workspace sizes) rebuilt with AddressSanitizer and
+    UndefinedBehaviorSanitizer on the host, linked with the kernels' objects of the regular build, and this file's
+    other tests run against it in a child process with the sanitizer runtime preloaded."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    objs = [os.path.join(root, "_build", f + ".o") for f in ("kv_tables.hip", "kv_append.hip", "kv_decode.hip",
+                                                             "kv_chunk.hip")]
+    if not all(os.path.exists(o) for o in objs):
+        pytest.skip("needs the kernel objects of the regular build (__graft_entry__.build())")
+    rts = glob.glob("/opt/rocm/llvm/lib/clang/*/lib/linux/libclang_rt.asan-x86_64.so")
+    if not rts:
+        pytest.skip("clang AddressSanitizer runtime not found")
+    hipcc = "/opt/rocm/bin/hipcc"
+    host_san = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=undefined",
+                "-Xarch_host", "-fno-omit-frame-pointer"]
+    mine, lib = str(tmp_path / "kv_api.o"), str(tmp_path / "libkm_cache_asan.so")
+    subprocess.run([hipcc, "-std=c++17", "-O1", "-g", "-fPIC", "--offload-arch=gfx950", *host_san,
+                    "-I", os.path.join(root, "include"), "-c",
+                    os.path.join(root, "means_clustering_amd", "csrc", "kv_api.cpp"), "-o", mine],
+                   check=True, capture_output=True)
+    subprocess.run([hipcc, "-shared", "-fPIC", "--offload-arch=gfx950", *host_san, "-shared-libasan", mine, *objs,
+                    "-o", lib], check=True, capture_output=True)
+    old = os.environ.get("LD_PRELOAD", "")
+    env = dict(os.environ, LD_PRELOAD=rts[0] + (":" + old if old else ""), ASAN_OPTIONS="detect_leaks=0",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+    r = subprocess.run([sys.executable, os.path.join(root, "tests", "native", "run_with_cache_lib.py"), lib,
+                        "-s", "-k", "not under_asan"], env=env, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-3000:]
+    assert "runtime error" not in r.stderr and "AddressSanitizer" not in r.stderr, r.stderr[-3000:]
