@@ -72,8 +72,8 @@ def lib():
             sig = {
                 "kmeans_kv_tables": (c_int, [vp, vp, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, vp,
                                              vp]),
-                "kmeans_kv_append": (c_int, [cache, c_int, i64, vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, f,
-                                             vp, vp, i64, i64, c_int, vp, vp, i64, i64, vp]),
+                "kmeans_kv_append": (c_int, [cache, c_int, i64, vp, i64, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp,
+                                             f, vp, vp, i64, i64, c_int, vp, vp, i64, i64, vp]),
                 "kmeans_kv_attend_workspace": (sz, [cache, i64, i64, i64, i64]),
                 "kmeans_kv_attend": (c_int, [cache, c_int, vp, i64, i64, i64, i64, vp, i64, i64, i64, vp, vp, vp, i64,
                                              i64, f, i64, i64, vp, i64, i64, vp, vp, sz, vp]),

@@ -14,4 +14,5 @@ import pytest  # noqa: E402
 from means_clustering_amd import kvcache  # noqa: E402
 
 kvcache.LIB_PATH = sys.argv[1]
-sys.exit(pytest.main([os.path.join(ROOT, "tests", "test_kvcache_abi.py"), "-q", "-p", "no:cacheprovider", *sys.argv[2:]]))
+tests = os.path.join(ROOT, "tests", "test_kvcache_abi.py")
+sys.exit(pytest.main([tests, "-q", "-p", "no:cacheprovider", *sys.argv[2:]]))

@@ -28,7 +28,8 @@ def _cache(**kw):
 
 
 def _append(L, cache=None, dt=km.KM_BF16, T=4, q=FAKE, hq=4, qs=(256, 64), k=FAKE, ks=(128, 64), v=FAKE,
-            vs=(128, 64), qw=None, kw=None, eps=1e-6, pos=FAKE, rope=FAKE, max_pos=100, rot=64, slots=FAKE, out=FAKE + 256,
+            vs=(128, 64), qw=None, kw=None, eps=1e-6,
+            pos=FAKE, rope=FAKE, max_pos=100, rot=64, slots=FAKE, out=FAKE + 256,
             os=(256, 64)):
     return L.kmeans_kv_append(cache or _cache(), dt, T, q, hq, *qs, k, *ks, v, *vs, qw, kw, eps, pos, rope, max_pos,
                               rot, 0, slots, out, *os, None)
@@ -117,7 +118,8 @@ def test_attend_limits_and_workspace(L):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(R=-1), dict(R=1 << 24), dict(T=-1), dict(p=8), dict(p=48), dict(width=-1), dict(stride=7), dict(width=1 << 27, stride=1 << 27),
+    dict(R=-1), dict(R=1 << 24), dict(T=-1), dict(p=8), dict(p=48), dict(width=-1), dict(stride=7),
+    dict(width=1 << 27, stride=1 << 27),
     dict(nf=-1), dict(qs=None), dict(ps=None), dict(ctx=None), dict(new=None), dict(seq=None), dict(table=None),
     dict(free=None), dict(pos=None), dict(slots=None), dict(ctx=ODD2), dict(off=ODD2), dict(slots=ODD2)], ids=str)
 def test_tables_refusals(L, bad):
