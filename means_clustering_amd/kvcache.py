@@ -153,7 +153,11 @@ def _table(t, index: int):
     stride, one = t.stride()
     if one != 1 and width > 1:
         raise ValueError("the rows of block_table must be contiguous")
-    return R, width, stride if stride > width else width
+    if stride < width:
+        if R > 1:
+            raise ValueError(f"the rows of block_table must not overlap (row stride {stride}, {width} columns)")
+        stride = width
+    return R, width, stride
 
 
 # The handle of a device's current stream (torch.cuda.current_stream would make a Stream object of it).

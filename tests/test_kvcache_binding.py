@@ -1,0 +1,30 @@
+"""Host-side rules of the cache binding that need no GPU."""
+import pytest
+import torch
+
+from means_clustering_amd import kvcache
+
+HOST = -1  # the device index of host tensors
+
+
+def test_block_table_rows_that_overlap_are_refused():
+    """A table shared by all requests as an expanded view has a row stride of 0: its rows do not lie `width` apart, and
+    reading them so would leave the buffer."""
+    shared = torch.zeros(8, dtype=torch.int32)
+    with pytest.raises(ValueError, match="overlap"):
+        kvcache._table(shared.expand(3, 8), HOST)
+    with pytest.raises(ValueError, match="overlap"):
+        kvcache._table(shared.as_strided((3, 4), (2, 1)), HOST)
+
+
+def test_block_table_strides():
+    big = torch.zeros(5, 12, dtype=torch.int32)
+    assert kvcache._table(big[:, :7], HOST) == (5, 7, 12)
+    assert kvcache._table(big[::2, :7], HOST) == (3, 7, 24)
+    assert kvcache._table(big[:, :0], HOST) == (5, 0, 12)
+    assert kvcache._table(big[:, 3:4], HOST) == (5, 1, 12)
+    # one row, or none: nothing lies a stride apart
+    assert kvcache._table(torch.zeros(8, dtype=torch.int32).as_strided((1, 8), (0, 1)), HOST) == (1, 8, 8)
+    assert kvcache._table(big[:0], HOST)[:2] == (0, 12)
+    with pytest.raises(ValueError, match="contiguous"):
+        kvcache._table(big.t(), HOST)
