@@ -163,8 +163,6 @@ def _table(t, index: int):
 # The handle of a device's current stream (torch.cuda.current_stream would make a Stream object of it).
 _stream = torch._C._cuda_getCurrentRawStream
 
-_default_ws: dict = {}  # one for each device and stream: calls on different streams may overlap
-
 
 def tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
            page_size: int, total: int, pos_offset: torch.Tensor | None = None) -> Tables:
@@ -251,6 +249,9 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     stands for, 0 for a token, -inf for none.  ``scale`` defaults to dim ** -0.5.  ``max_new`` bounds the new tokens
     of any request (1 in a decode step).  ``lse`` True or an fp32 [T, q_heads] tensor also gives the logarithm of each
     row's sum.  Returns out, or (out, lse).
+
+    Without ``ws`` each call takes its workspace from torch's allocator, so calls of several threads and calls that a
+    graph captures share nothing.  A ``ws`` serves one stream of calls at a time.
     """
     cache = _cache(k_cache, v_cache)
     dev, dt = k_cache.get_device(), k_cache.dtype
@@ -277,16 +278,16 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
         max_new = T
     L, stream = lib(), _stream(dev)
     if ws is None:
-        ws = _default_ws.get((dev, stream))
-        if ws is None:
-            ws = _default_ws.setdefault((dev, stream), Workspace())
-    buf = ws.buf if ws.buf is not None and ws.buf.get_device() == dev else None
+        # (freed at the end: the allocator gives it to later work of this stream only, a graph's stays the graph's)
+        buf = q.new_empty(L.kmeans_kv_attend_workspace(cache, T, hq, R, max_new), dtype=torch.uint8)
+    else:
+        buf = ws.buf if ws.buf is not None and ws.buf.get_device() == dev else None
     for _ in range(2):
         status = L.kmeans_kv_attend(cache, _DT[dt], q.data_ptr(), T, hq, qs[0], qs[1], block_table.data_ptr(), R, width,
                                     tstride, starts, lens, _ptr(log_weight), lw_page, lw_head,
                                     cache.dim ** -0.5 if scale is None else scale, window, max_new, out.data_ptr(),
                                     os_[0], os_[1], l, _ptr(buf), 0 if buf is None else buf.numel(), stream)
-        if status != KM_ERR_WORKSPACE:
+        if status != KM_ERR_WORKSPACE or ws is None:
             break
         # the first call, or a larger one than before (the workspace is the last argument to be refused)
         buf = ws.get(L.kmeans_kv_attend_workspace(cache, T, hq, R, max_new), q.device)
