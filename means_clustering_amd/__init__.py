@@ -118,17 +118,29 @@ def workspace_bytes(op: int, N: int, D: int, K: int, dtype=torch.bfloat16, chunk
 
 
 class Workspace:
-    """A reusable device scratch buffer for the library's calls."""
+    """A reusable device scratch buffer for the library's calls.
+
+    It grows with the calls that use it.  A buffer that a captured graph uses is kept as long as the Workspace, which
+    therefore has to live as long as the graph; replays share it with every other call, so one at a time.
+    """
 
     def __init__(self, device=None):
         self.device = torch.device(device) if device is not None else None
         self.buf = None
+        self.captured = []  # buffers whose address a graph holds
 
     def get(self, nbytes: int, device) -> torch.Tensor:
         nbytes = max(int(nbytes), 256)
         if self.buf is None or self.buf.numel() < nbytes or self.buf.device != torch.device(device):
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if self.buf.is_cuda and torch.cuda.is_current_stream_capturing():
+            self.hold()
         return self.buf
+
+    def hold(self):
+        """Keeps the present buffer, also when a larger one takes its place."""
+        if all(b is not self.buf for b in self.captured):
+            self.captured.append(self.buf)
 
 
 _default_ws: dict = {}

@@ -251,7 +251,8 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     row's sum.  Returns out, or (out, lse).
 
     Without ``ws`` each call takes its workspace from torch's allocator, so calls of several threads and calls that a
-    graph captures share nothing.  A ``ws`` serves one stream of calls at a time.
+    graph captures share nothing.  A ``ws`` serves one stream of calls at a time; graphs that captured it have to be
+    gone before it is.
     """
     cache = _cache(k_cache, v_cache)
     dev, dt = k_cache.get_device(), k_cache.dtype
@@ -282,6 +283,8 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
         buf = q.new_empty(L.kmeans_kv_attend_workspace(cache, T, hq, R, max_new), dtype=torch.uint8)
     else:
         buf = ws.buf if ws.buf is not None and ws.buf.get_device() == dev else None
+        if buf is not None and torch.cuda.is_current_stream_capturing():
+            ws.hold()
     for _ in range(2):
         status = L.kmeans_kv_attend(cache, _DT[dt], q.data_ptr(), T, hq, qs[0], qs[1], block_table.data_ptr(), R, width,
                                     tstride, starts, lens, _ptr(log_weight), lw_page, lw_head,

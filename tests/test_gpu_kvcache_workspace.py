@@ -128,3 +128,32 @@ def test_graph_without_a_workspace_outlives_larger_calls():
         kvcache.attend(**large)
         torch.cuda.synchronize()
         assert all(bool((f == 7).all()) for f in filled)
+
+
+def test_graph_with_a_workspace_that_grows_later():
+    """The captured buffer stays with the Workspace: memory taken after a larger call is not the graph's."""
+    small, large = _inputs(SHAPES[0]), _inputs(SHAPES[2], seed=3)
+    ws = kvcache.Workspace(DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        want, wl = kvcache.attend(**small, lse=True, ws=ws)
+    s.synchronize()
+    first = ws.buf.data_ptr()
+    graph, (got, gl) = _capture(s, small, ws=ws)
+    assert [b.data_ptr() for b in ws.captured] == [first]
+    with torch.cuda.stream(s):
+        want_large, _ = kvcache.attend(**large, lse=True, ws=ws)
+    s.synchronize()
+    assert ws.buf.data_ptr() != first and [b.data_ptr() for b in ws.captured] == [first]
+    filled = _fill()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got.zero_(), gl.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+        assert torch.equal(kvcache.attend(**large, ws=ws), want_large)
+        torch.cuda.synchronize()
+        assert all(bool((f == 7).all()) for f in filled)

@@ -1,4 +1,6 @@
 """Host-side rules of the cache binding that need no GPU."""
+import weakref
+
 import pytest
 import torch
 
@@ -28,3 +30,16 @@ def test_block_table_strides():
     assert kvcache._table(big[:0], HOST)[:2] == (0, 12)
     with pytest.raises(ValueError, match="contiguous"):
         kvcache._table(big.t(), HOST)
+
+
+def test_workspace_keeps_held_buffers():
+    """A buffer whose address a graph holds outlives the growth of its Workspace; others are freed."""
+    ws = kvcache.Workspace("cpu")
+    first = weakref.ref(ws.get(1000, "cpu"))
+    ws.hold(), ws.hold()
+    second = weakref.ref(ws.get(2000, "cpu"))
+    ws.get(3000, "cpu")
+    assert first() is not None and second() is None and len(ws.captured) == 1
+    assert ws.buf.numel() == 3000
+    del ws
+    assert first() is None
