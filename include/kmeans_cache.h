@@ -73,7 +73,8 @@ typedef struct km_kv_cache {
  * T is the capacity of positions and slots.  Tokens beyond the total get
  * position 0 and slot -1; tokens that find no room (free list or table row
  * exhausted: page_start[R] > num_free, or need > width) get slot -1 and their
- * table entries -1.  Sums of lengths must stay below 2^31.  Limits: R < 2^24;
+ * table entries -1.  Tokens in a page that no cache can have (negative, or
+ * 2^31 / page_size or more) get slot -1.  Sums of lengths must stay below 2^31.  Limits: R < 2^24;
  * width * page_size < 2^31.
  */
 km_status kmeans_kv_tables(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* pos_offset, int64_t R,

@@ -138,7 +138,9 @@ __global__ __launch_bounds__(kThreads) void tables_kernel(TablesArgs a) {
         }
       }
       pos = at + (a.offset ? a.offset[r] : 0);
-      if (page >= 0) slot = (page << a.page_shift) + (at & ((1 << a.page_shift) - 1));
+      // (the slots of a page beyond the last whole one below 2^31 would wrap into another's)
+      if (page >= 0 && page < (1 << (31 - a.page_shift)))
+        slot = (page << a.page_shift) + (at & ((1 << a.page_shift) - 1));
     }
     a.positions[t] = pos;
     a.slots[t] = slot;
