@@ -299,8 +299,9 @@ extern "C" km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, con
   a.Hkv = (int32_t)cache->heads;
   a.G = (int32_t)(q_heads / cache->heads);
   a.D = (int32_t)cache->dim;
-  // a window of the whole cache is none
-  a.window = window >= width * cache->page_size ? 0 : (int32_t)window;
+  // A window of more than every position (at most 2^30) is none.  (Not one of the table row's room: a request that is
+  // longer than its row has queries beyond it, from which the window hides slots of the row.)
+  a.window = window >= kMaxRoom ? 0 : (int32_t)window;
   a.scale = log_weight ? scale : scale * 1.4426950408889634f;
   uint8_t* base = (uint8_t*)ws;
   a.per_head = (int64_t*)(base + p.head_at);

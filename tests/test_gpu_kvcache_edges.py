@@ -38,3 +38,27 @@ def test_tables_pages_that_no_cache_can_have(p):
         cache = torch.zeros(4, p, 1, 16, dtype=BF, device=DEV)
         kvcache.append(None, torch.ones(4 * R, 1, 16, dtype=BF, device=DEV), None, cache, None, t.slots)
         assert bool((cache[2, :4] == 1).all()) and float(cache.float().sum()) == 4 * 16
+
+
+# ------------------------------------------------------------------------------------------------------ attend ----
+
+def _check(c, **changes):
+    """The call against Case.reference, its tolerances and its rule for rows that see nothing."""
+    out, lse = kvcache.attend(**dict(c.device(), **changes), lse=True)
+    torch.cuda.synchronize()
+    ro, rl, to, tl = c.reference()
+    got, gl = out.double().cpu(), lse.double().cpu()
+    assert bool(((got - ro).abs() <= to).all()), ((got - ro).abs() - to).max()
+    empty = rl == -math.inf
+    assert bool((gl[empty] == -math.inf).all()) and bool((got[empty] == 0).all())
+    assert bool(((gl[~empty] - rl[~empty]).abs() <= tl[~empty]).all())
+
+
+@pytest.mark.parametrize("n", [1, 12, 60])
+@pytest.mark.parametrize("window", [63, 64, 65, 80, 100, 5000, 2 ** 31 - 1])
+def test_attend_window_over_a_row_shorter_than_its_request(n, window):
+    """100 slots, of which the table row holds 64: the last query stands at slot 99 and sees those after 99 - window."""
+    c = Case([(100, n), (70, 1)], 4, 2, 64, BF, window=window)
+    c.table[:, 4:] = -1
+    print(f"[attend] n={n} window={window}", flush=True)
+    _check(c, block_table=c.table[:, :4].contiguous().to(DEV))
