@@ -138,7 +138,10 @@ size_t kmeans_kv_attend_workspace(const km_kv_cache* cache, int64_t T, int64_t q
  *   lse         device fp32[T x q_heads] or NULL
  *   max_new     no request has more new tokens (T always serves)
  * Slots beyond seq_lens[r] or width * page_size and slots of pages outside
- * [0, pages) are not seen.  A row that sees nothing is zero, its lse -inf.
+ * [0, pages) are not seen.  Of a request whose tokens pass T the first ones
+ * are answered, at the slots that they have among all of them.  Rows of a
+ * request with more than max_new new tokens are left as they are or hold
+ * anything.  A row that sees nothing is zero, its lse -inf.
  * What a row does not see never reaches it, whatever it holds (infinities and
  * NaN too).  Rows of tokens outside every request are not written.  Scores,
  * softmax and sums are fp32; the softmax terms are rounded to dt for the

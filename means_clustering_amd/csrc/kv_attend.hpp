@@ -37,7 +37,8 @@ __device__ __forceinline__ int first_key(const AttendArgs& a, int p) {
 
 struct Request {
   int q0, n;   // first query token, query tokens
-  int seq, c;  // slots in the cache, slot of the first query (below 0 where there are more queries than slots)
+  int seq, c;  // slots that its queries can see, slot of the first query (below 0 where there are more queries than
+               // slots)
   int tiles;   // 0: not of this launch
   int units;   // key units of its longest tile, at least 1
 };
@@ -45,12 +46,14 @@ struct Request {
 template <int BM, int UNIT>
 __device__ __forceinline__ Request request_of(const AttendArgs& a, int r) {
   Request q;
+  const int end = a.query_start[r + 1];
   q.q0 = clampi(a.query_start[r], 0, a.T);
-  q.n = clampi(a.query_start[r + 1], q.q0, a.T) - q.q0;
+  q.n = clampi(end, q.q0, a.T) - q.q0;
   // (room is at most 2^30: positions and keys stay far from the ends of 32 bits)
   const int room = a.width << a.page_shift, sl = clampi(a.seq_lens[r], 0, 1 << 30);
-  q.seq = min(sl, room);
-  q.c = sl - q.n;
+  // (of more new tokens than T the first ones are here, and stand where they would with all)
+  q.c = sl - min(max(end, q.q0) - q.q0, 1 << 30);
+  q.seq = min(min(sl, q.c + q.n), room);
   const int64_t rows = (int64_t)q.n * a.G;
   q.tiles = rows > a.lo_rows && rows <= a.hi_rows ? (int)((rows + BM - 1) / BM) : 0;
   int64_t keys = q.seq;

@@ -62,3 +62,47 @@ def test_attend_window_over_a_row_shorter_than_its_request(n, window):
     c.table[:, 4:] = -1
     print(f"[attend] n={n} window={window}", flush=True)
     _check(c, block_table=c.table[:, :4].contiguous().to(DEV))
+
+
+@pytest.mark.parametrize("last,kept", [(30, 1), (30, 15), (3, 2), (90, 40), (90, 89)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_attend_request_cut_off_by_the_capacity(last, kept, window):
+    """query_start passes T: the last request's first tokens keep their slots, and the slots of the others, which
+    nobody wrote, are not read."""
+    c = Case([(50, 20), (120, last)], 4, 2, 64, BF, window=window)
+    ro, rl, to, tl = c.reference()
+    for j in range(120 - last + kept, 120):
+        c.set(1, j, k=math.nan, v=math.nan)
+    d, T = c.device(), 20 + kept
+    print(f"[attend] last={last} kept={kept} window={window}", flush=True)
+    out, lse = kvcache.attend(**dict(d, q=d["q"][:T].contiguous(), max_new=max(20, last)), lse=True)
+    assert bool(((out.double().cpu() - ro[:T]).abs() <= to[:T]).all())
+    assert bool(((lse.double().cpu() - rl[:T]).abs() <= tl[:T]).all())
+
+
+def test_step_with_more_tokens_than_the_capacity():
+    """tables, append and attend with `total` below the sum of the new lengths: the tokens that have rows are answered
+    as if all were there."""
+    g = torch.Generator().manual_seed(4)
+    p, hq, h, D = 16, 4, 2, 64
+    ctx, new, cap = [40, 21], [6, 50], 33
+    rows = torch.randn(56, hq + 2 * h, D, generator=g).to(BF).to(DEV)
+
+    def step(total):
+        k = torch.full((16, p, h, D), math.nan, dtype=BF, device=DEV)
+        v = k.clone()
+        old = torch.randn(2, 48, h, D, generator=torch.Generator().manual_seed(5)).to(BF).to(DEV)
+        table = torch.full((2, 8), -1, dtype=torch.int32, device=DEV)
+        table[0, :3], table[1, :2] = _i32([1, 2, 3]), _i32([5, 6])
+        for r, c in enumerate(ctx):
+            at = torch.arange(c, device=DEV)
+            k[table[r].long()[at // p], at % p] = v[table[r].long()[at // p], at % p] = old[r, :c]
+        t = kvcache.tables(_i32(ctx), _i32(new), table, _i32(list(range(8, 16))), p, total)
+        x = rows[:total]
+        q = kvcache.append(x[:, :hq], x[:, hq:hq + h], x[:, hq + h:], k, v, t.slots)
+        return kvcache.attend(q, k, v, table, t.query_start, t.seq_lens, lse=True)
+
+    (whole, wl), (cut, cl) = step(56), step(cap)
+    # both round the terms and the result (2^-8 each) of values of at most |v|
+    assert float((whole[:cap].float() - cut.float()).abs().max()) <= 4 * 2.0 ** -8 * float(rows[:, hq + h:].abs().max())
+    assert float((wl[:cap] - cl).abs().max()) <= 1e-4
