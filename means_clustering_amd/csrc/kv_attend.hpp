@@ -302,6 +302,14 @@ __device__ __forceinline__ float sum16(float x) {
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// A product that is rounded by itself.  (Scores and their maximum: were one of
+// them part of a fused difference, a maximum of 2^28 could be 16 below its own
+// score, whose term 2^16 is more than fp16 holds.)
+__device__ __forceinline__ float product(float x, float y) {
+#pragma clang fp contract(off)
+  return x * y;
+}
+
 // Scores are in units of log 2, so that 2^(s - m) takes no product; with
 // weights they are natural, since log2(e) times a weight of the type's lowest
 // value would overflow (a row of such keys is their plain mean, and its lse

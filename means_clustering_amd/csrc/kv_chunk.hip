@@ -281,7 +281,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
 #pragma unroll
       for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
     mx = max32(mx);
-    if (!LW) mx *= scale;
+    if (!LW) mx = product(mx, scale);
     const float mn = fmaxf(m_, mx), ms = mn == -INFINITY ? 0.f : mn;
     if (__any(mn > m_)) {
       const float al = factor<LW>(m_, ms);
@@ -291,6 +291,16 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= al;
       m_ = mn;
+    }
+    // the exponent of a term is score * factor + base; from 2^24 on the maximum's rounding shows in a fused sum (product())
+    float fac = scale, base = -ms;
+    if (!LW && __any(fabsf(ms) >= 16777216.f)) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[t][i] = product(s[t][i], scale) - ms;
+      fac = 1.f;
+      base = 0.f;
     }
     float sum = 0.f;
     auto values = [&](int u, u32x4_t(&vf)[DT]) __attribute__((always_inline)) {
@@ -308,7 +318,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
     auto terms = [&](int u, u32x4_t& pf) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float v = s[u / 2][8 * (u & 1) + j], e = LW ? factor<LW>(v, ms) : exp2_(fmaf(v, scale, -ms));
+        const float v = s[u / 2][8 * (u & 1) + j], e = LW ? factor<LW>(v, ms) : exp2_(fmaf(v, fac, base));
         s[u / 2][8 * (u & 1) + j] = e;
         sum += e;
       }

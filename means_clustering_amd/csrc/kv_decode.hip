@@ -234,7 +234,7 @@ __global__ __launch_bounds__(kWgThreads, decode_per_cu(DP, 16 * NQ)) void decode
           for (int kb = 0; kb < KB; ++kb) acc = mfma16<T>(t.k[h][kb], qf[q][kb], acc);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float v = acc[i] * a.scale;
+            float v = product(acc[i], a.scale);
             if (LW) v = t.w[h][i] == -INFINITY ? -INFINITY : v + t.w[h][i];  // (whatever the key is)
             s[4 * h + i] = v;
           }

@@ -107,3 +107,21 @@ def test_step_with_more_tokens_than_the_capacity():
     most = max(float(rows[:, hq + h:].abs().max()), float(old.abs().max()))
     assert float((whole[:cap].float() - cut.float()).abs().max()) <= 4 * 2.0 ** -8 * most
     assert float((wl[:cap] - cl).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("n", [1, 90])
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_attend_scores_of_any_size(dt, n, weighted):
+    """Scores from thousands to 2^31: no term leaves the type, whatever the scores' own rounding makes of them."""
+    for size in (4.0, 64.0, 512.0, 2048.0, 4096.0, 16384.0):
+        c = Case([(300, n)], 4, 2, 64, dt, weighted=weighted, sharp=size)
+        c.k = torch.where(torch.isnan(c.k), c.k, (c.k.float() * size).clamp(-65504, 65504).to(dt))
+        c.q = (c.q.float().nan_to_num(posinf=65504.0, neginf=-65504.0)).to(dt)  # (fp16: randn beyond 4 has overflowed)
+        c.scale = 1.0
+        out, lse = kvcache.attend(**c.device(), lse=True)
+        seen = c.v[torch.isfinite(c.v)].abs().max()
+        assert bool(torch.isfinite(out).all()) and float(out.abs().max()) <= 1.01 * float(seen)
+        want = c.reference()[1]
+        bound = 80 * E * float(c.q.double().abs().max()) * float(c.k[torch.isfinite(c.k)].double().abs().max()) * 64
+        assert bool(((lse.double().cpu() - want).abs() <= bound + 1e-4).all())
