@@ -145,7 +145,10 @@ size_t kmeans_kv_attend_workspace(const km_kv_cache* cache, int64_t T, int64_t q
  * What a row does not see never reaches it, whatever it holds (infinities and
  * NaN too).  Rows of tokens outside every request are not written.  Scores,
  * softmax and sums are fp32; the softmax terms are rounded to dt for the
- * product with the values.  Results do not depend on scheduling.
+ * product with the values: to 8 bits in KM_BF16; in KM_F16 to 11 bits, fewer
+ * below 2^-28 and none below 2^-39 of the row's largest so far.  (So a visible
+ * infinite value whose term is 0 can make its row NaN.)  Results do not depend
+ * on scheduling.
  * Limits: q_heads a multiple of heads; T, R < 2^24; T * q_heads < 2^31; width *
  * page_size <= 2^30; (R + T * q_heads / heads / 128) * heads below about 2^24
  * (beyond: KM_ERR_UNSUPPORTED).

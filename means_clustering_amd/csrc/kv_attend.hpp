@@ -318,10 +318,19 @@ template <bool NAT>
 __device__ __forceinline__ float factor(float s, float m) {
   return exp2_(NAT ? (s - m) * kLog2e : s - m);
 }
-// The natural logarithm of l terms relative to m.
-template <bool NAT>
+// The softmax term of a score, times 2^kTerm.
+template <class T, bool NAT>
+__device__ __forceinline__ float term(float s, float m) {
+  if constexpr (T::kTerm == 0.f)
+    return factor<NAT>(s, m);
+  else
+    return exp2_(NAT ? fmaf(s - m, kLog2e, T::kTerm) : (s - m) + T::kTerm);
+}
+// The natural logarithm of a sum l of terms relative to m.
+template <class T, bool NAT>
 __device__ __forceinline__ float log_sum(float m, float l) {
-  return NAT ? m + __log2f(l) * kLn2 : (m + __log2f(l)) * kLn2;
+  const float e = __log2f(l * __builtin_ldexpf(1.f, -(int)T::kTerm));
+  return NAT ? m + e * kLn2 : (m + e) * kLn2;
 }
 
 // Whether an element of the packed pair is infinite or NaN.

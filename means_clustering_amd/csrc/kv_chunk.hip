@@ -293,14 +293,14 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
       m_ = mn;
     }
     // the exponent of a term is score * factor + base; from 2^24 on the maximum's rounding shows in a fused sum (product())
-    float fac = scale, base = -ms;
+    float fac = scale, base = T::kTerm - ms;
     if (!LW && __any(fabsf(ms) >= 16777216.f)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[t][i] = product(s[t][i], scale) - ms;
       fac = 1.f;
-      base = 0.f;
+      base = T::kTerm;
     }
     float sum = 0.f;
     auto values = [&](int u, u32x4_t(&vf)[DT]) __attribute__((always_inline)) {
@@ -318,7 +318,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
     auto terms = [&](int u, u32x4_t& pf) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float v = s[u / 2][8 * (u & 1) + j], e = LW ? factor<LW>(v, ms) : exp2_(fmaf(v, fac, base));
+        const float v = s[u / 2][8 * (u & 1) + j], e = LW ? term<T, LW>(v, ms) : exp2_(fmaf(v, fac, base));
         s[u / 2][8 * (u & 1) + j] = e;
         sum += e;
       }
@@ -427,7 +427,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
           *(u32x2_t*)(op + e) = u32x2_t{T::pack(o[d][4 * b] * inv, o[d][4 * b + 1] * inv),
                                         T::pack(o[d][4 * b + 2] * inv, o[d][4 * b + 3] * inv)};
       }
-    if (a.lse && h == 0) a.lse[tok * a.Hq + hq] = log_sum<LW>(ms, L);
+    if (a.lse && h == 0) a.lse[tok * a.Hq + hq] = log_sum<T, LW>(ms, L);
   } else {
     const int64_t at = ((int64_t)w.part() * a.Hkv + head) * BM + 32 * wave + x;
 #pragma unroll

@@ -35,7 +35,10 @@
 //     Keys are not: a load takes half of each line, so the other half is
 //     wanted at once (both so: 164 us, a third more reads of the L2).
 // P is rounded to the cache's type for the matrix cores: its relative error of
-// 2^-8 (2^-11) is that of the result's own rounding.  m, l and o are fp32.
+// 2^-8 (2^-11) is that of the result's own rounding.  In fp16 the terms are
+// held times 2^14, or those below 2^-14 of the largest would lose bits and
+// those below 2^-25 everything, though a long context can have most of its sum
+// in them; so 2^-28 and 2^-39 are the limits.  m, l and o are fp32.
 #include "kv_attend.hpp"
 
 namespace kmkv {
@@ -255,7 +258,7 @@ __global__ __launch_bounds__(kWgThreads, decode_per_cu(DP, 16 * NQ)) void decode
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          s[j] = factor<LW>(s[j], ms);
+          s[j] = term<T, LW>(s[j], ms);
           sum += s[j];
         }
         m_[q] = mn;
@@ -374,7 +377,7 @@ __global__ __launch_bounds__(kWgThreads, decode_per_cu(DP, 16 * NQ)) void decode
         if (d < a.D)
           *(u32x2_t*)(a.out + tok * a.o_token + hq * a.o_head + d) =
               u32x2_t{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
-        if (a.lse && d == 0) a.lse[tok * a.Hq + hq] = log_sum<LW>(ms, L);
+        if (a.lse && d == 0) a.lse[tok * a.Hq + hq] = log_sum<T, LW>(ms, L);
       } else {
         const int64_t at = (int64_t)part * BM + m;
         *(f32x4_t*)(a.part_o + at * DP + d) = acc;
@@ -486,7 +489,7 @@ __global__ __launch_bounds__(kWgThreads) void join_kernel(JoinArgs a) {
   const float inv = L == 0.f ? 0.f : 1.0f / L;
   *(u32x2_t*)(a.out + t * a.o_token + hq * a.o_head + d) =
       u32x2_t{T::pack(acc[0] * inv, acc[1] * inv), T::pack(acc[2] * inv, acc[3] * inv)};
-  if (a.lse && d == 0) a.lse[(int64_t)t * a.Hq + hq] = log_sum<LW>(M == -INFINITY ? 0.f : M, L);
+  if (a.lse && d == 0) a.lse[(int64_t)t * a.Hq + hq] = log_sum<T, LW>(M == -INFINITY ? 0.f : M, L);
 }
 
 template <class T, int DP, int NQ, bool LW>

@@ -20,10 +20,13 @@ typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 // 16-bit element types: two elements packed in 32 bits, widened or rounded
-// (to nearest, ties to even), and what an element's exponent looks like when
-// it is infinite or NaN.
+// (to nearest, ties to even), what an element's exponent looks like when it is
+// infinite or NaN, and the power of two that softmax terms are held times, so
+// that those far below the largest (which is 1 before) keep their bits: fp16
+// has full ones down to 2^-14 and none below 2^-25.
 struct BF16 {
   static constexpr uint32_t kExp = 0x7f80u;
+  static constexpr float kTerm = 0.f;
   static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
   static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
   static __device__ __forceinline__ uint32_t pack(float a, float b) {
@@ -32,6 +35,7 @@ struct BF16 {
 };
 struct F16 {
   static constexpr uint32_t kExp = 0x7c00u;
+  static constexpr float kTerm = 14.f;
   static __device__ __forceinline__ float lo(uint32_t w) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)(w & 0xffffu));
   }

@@ -125,3 +125,42 @@ def test_attend_scores_of_any_size(dt, n, weighted):
         want = c.reference()[1]
         bound = 80 * E * float(c.q.double().abs().max()) * float(c.k[torch.isfinite(c.k)].double().abs().max()) * 64
         assert bool(((lse.double().cpu() - want).abs() <= bound + 1e-4).all())
+
+
+def _sink(keys, n, hkv, R, at, weighted):
+    """Requests over one set of pages whose slot `at` has a score 18 (e^18 is 2^26) above the others', and a value of
+    zero: the result is made of terms near 2^-26 of the largest."""
+    g = torch.Generator().manual_seed(keys + n + at)
+    D, p = 64, 64
+    k = (0.3 * torch.randn(keys, hkv, D, generator=g)).half()
+    v = (1 + 0.1 * torch.randn(keys, hkv, D, generator=g)).half()
+    k[at], v[at] = 0, 0
+    k[at, :, 0] = 18
+    q = (0.5 * torch.randn(R * n, hkv, D, generator=g)).half()
+    q[..., 0] = 8
+    table = torch.arange(keys // p, dtype=torch.int32).repeat(R, 1)
+    d = dict(q=q.to(DEV), k_cache=k.view(-1, p, hkv, D).to(DEV), v_cache=v.view(-1, p, hkv, D).to(DEV),
+             block_table=table.to(DEV), query_start=_i32([n * r for r in range(R + 1)]), seq_lens=_i32([keys] * R),
+             scale=0.125, max_new=n,
+             log_weight=torch.zeros(keys // p, hkv, p, device=DEV) if weighted else None)
+    sc = 0.125 * q.double().transpose(0, 1) @ k.double().permute(1, 2, 0)
+    es = (D + 16) * E * 0.125 * (q.double().abs().transpose(0, 1) @ k.double().abs().permute(1, 2, 0)).amax(2)
+    i = torch.arange(R * n) % n
+    sc.masked_fill_(torch.arange(keys)[None, None] > (keys - n + i)[None, :, None], -math.inf)
+    pr, vv = torch.softmax(sc, 2), v.double().transpose(0, 1)
+    # fp16 terms hold 2^-39 of the largest; the result's own step is 2^-24 below 2^-14
+    tol = (2.1 * U[FP] + 4 * es + (keys / 32 + 64) * E)[..., None] * (pr @ vv.abs()) + (
+        keys * 2.0 ** -39 * float(vv.abs().max()) + 2.0 ** -25)
+    lse = torch.logsumexp(sc, 2)
+    return d, (pr @ vv).transpose(0, 1), tol.transpose(0, 1), lse.t(), (es + (keys / 32 + 64) * E + 4 * E * lse.abs()).t()
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("keys,n,hkv,R,at", [(4096, 1, 8, 96, 0), (4096, 1, 8, 96, 4000), (4096, 20, 2, 9, 7),
+                                             (16384, 256, 8, 1, 0), (16384, 256, 8, 1, 16000), (2048, 128, 4, 64, 3)])
+def test_attend_fp16_terms_far_below_the_largest(keys, n, hkv, R, at, weighted):
+    d, want, tol, wl, ltol = _sink(keys, n, hkv, R, at, weighted)
+    print(f"[attend] keys={keys} n={n} hkv={hkv} R={R} at={at} weighted={weighted}", flush=True)
+    out, lse = kvcache.attend(**d, lse=True)
+    assert bool(((out.double().cpu() - want).abs() <= tol).all())
+    assert bool(((lse.double().cpu() - wl).abs() <= ltol).all())
