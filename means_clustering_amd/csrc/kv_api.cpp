@@ -249,7 +249,9 @@ extern "C" km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, con
   if (dt == KM_F32) return fail(KM_ERR_UNSUPPORTED, "the cache holds KM_BF16 or KM_F16");
   if (dt != KM_BF16 && dt != KM_F16) return invalid("dtype must be KM_BF16 or KM_F16");
   if (window < 0 || window > kMaxI) return invalid("window must be 0 (none) to 2^31 - 1");
-  if (!(scale - scale == 0.f)) return invalid("scale must be finite");
+  // (without weights the scores are in units of log 2)
+  const float unit = log_weight ? scale : scale * 1.4426950408889634f;
+  if (!(unit - unit == 0.f)) return invalid("scale must be finite, times log2(e) too");
   if (width < 0 || width > kMaxRoom / cache->page_size || table_stride < width || table_stride >= kMaxStride)
     return invalid("width must be at least 0, width * page_size at most 2^30 and table_stride at least width");
   if (T == 0 || R == 0 || max_new == 0) return KM_OK;
@@ -302,7 +304,7 @@ extern "C" km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, con
   // A window of more than every position (at most 2^30) is none.  (Not one of the table row's room: a request that is
   // longer than its row has queries beyond it, from which the window hides slots of the row.)
   a.window = window >= kMaxRoom ? 0 : (int32_t)window;
-  a.scale = log_weight ? scale : scale * 1.4426950408889634f;
+  a.scale = unit;
   uint8_t* base = (uint8_t*)ws;
   a.per_head = (int64_t*)(base + p.head_at);
   a.info = (int4*)(base + p.info_at);

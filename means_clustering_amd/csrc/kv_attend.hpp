@@ -338,6 +338,11 @@ template <class T>
 __device__ __forceinline__ bool odd_pair(uint32_t w) {
   return (w & T::kExp) == T::kExp || ((w >> 16) & T::kExp) == T::kExp;
 }
+// The pair times 0: NaN for such elements.
+template <class T>
+__device__ __forceinline__ uint32_t zero_pair(uint32_t w) {
+  return ((w & T::kExp) == T::kExp ? 0x7fffu : 0u) | (((w >> 16) & T::kExp) == T::kExp ? 0x7fff0000u : 0u);
+}
 // The pair with such elements replaced by 0.
 template <class T>
 __device__ __forceinline__ uint32_t even_pair(uint32_t w) {

@@ -107,7 +107,8 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
   // this lane's query row
   const int m = w.tile * BM + 32 * wave + x, mc = min(m, rows - 1);
   const int qi = mc / a.G, hq = head * a.G + (mc - qi * a.G);
-  const float scale = fmaxf(fabsf(a.scale), 1e-30f);  // (above 0, so that the largest product is the largest score)
+  // (above 0, so that the largest product is the largest score; a scale of 0 makes zeros of the queries instead)
+  const float scale = a.scale == 0.f ? 1.f : fabsf(a.scale);
   u32x4_t qf[KB];
   {
     const uint16_t* qp = a.q + (int64_t)(w.q.q0 + qi) * a.q_token + hq * a.q_head + 8 * h;
@@ -116,6 +117,10 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
     for (int kb = 0; kb < KB; ++kb) {
       qf[kb] = u32x4_t{0u, 0u, 0u, 0u};
       if (16 * kb + 8 * h < a.D) qf[kb] = *(const u32x4_t*)(qp + 16 * kb) ^ sign;
+      if (a.scale == 0.f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) qf[kb][i] = zero_pair<T>(qf[kb][i]);
+      }
     }
   }
   const int jmax = min(c + qi, k1 - 1), jmin = a.window > 0 ? c + qi - a.window + 1 : 0;

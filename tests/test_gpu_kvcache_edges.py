@@ -44,7 +44,10 @@ def test_tables_pages_that_no_cache_can_have(p):
 
 def _check(c, **changes):
     """The call against Case.reference, its tolerances and its rule for rows that see nothing."""
-    out, lse = kvcache.attend(**dict(c.device(), **changes), lse=True)
+    _near(c, *kvcache.attend(**dict(c.device(), **changes), lse=True))
+
+
+def _near(c, out, lse):
     torch.cuda.synchronize()
     ro, rl, to, tl = c.reference()
     got, gl = out.double().cpu(), lse.double().cpu()
@@ -164,3 +167,30 @@ def test_attend_fp16_terms_far_below_the_largest(keys, n, hkv, R, at, weighted):
     out, lse = kvcache.attend(**d, lse=True)
     assert bool(((out.double().cpu() - want).abs() <= tol).all())
     assert bool(((lse.double().cpu() - wl).abs() <= ltol).all())
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("n", [1, 90])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-35, -1e-35, 1e-40, -0.125])
+def test_attend_scales(scale, n, weighted):
+    """Products of 2^100: a scale of 0 makes every score 0, tiny ones (a denormal too) count as they are."""
+    c = Case([(150, n), (40, n if n < 40 else 40)], 4, 2, 64, BF, weighted=weighted)
+    if abs(scale) < 0.1:
+        c.q, c.k = (c.q.float() * 2.0 ** 50).to(BF), (c.k.float() * 2.0 ** 50).to(BF)
+    c.scale = scale
+    out, lse = kvcache.attend(**c.device(), lse=True)
+    c.scale = abs(scale)  # (the reference takes its tolerance times the scale)
+    if scale < 0:
+        c.q = -c.q
+    _near(c, out, lse)
+
+
+@pytest.mark.parametrize("n", [1, 90])
+def test_attend_scale_of_zero_with_infinite_queries(n):
+    """0 times an infinite product is NaN in the row that has it, and in no other."""
+    c = Case([(150, n), (40, 1)], 4, 2, 64, BF)
+    c.q[0, 1, 3] = math.inf
+    c.scale = 0.0
+    out = kvcache.attend(**c.device())
+    nan = torch.isnan(out)
+    assert bool(nan[0, 1].all()) and int(nan.sum()) == 64

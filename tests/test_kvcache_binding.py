@@ -6,6 +6,8 @@ import torch
 
 from means_clustering_amd import kvcache
 
+from .test_kvcache_abi import FAKE, _attend, _said
+
 HOST = -1  # the device index of host tensors
 
 
@@ -43,3 +45,10 @@ def test_workspace_keeps_held_buffers():
     assert ws.buf.numel() == 3000
     del ws
     assert first() is None
+
+
+def test_scale_that_overflows_in_units_of_log_2():
+    L = kvcache.lib()
+    assert _attend(L, scale=3e38) == 1 and "scale" in _said(L)
+    assert _attend(L, scale=-3e38) == 1
+    assert _attend(L, scale=3e38, lw=FAKE, ws=None, nb=0) == 3  # (with weights they are natural: only the workspace lacks)
