@@ -15,6 +15,8 @@ Entry points (all tensors on one ROCm device):
 
 Caches are 4-d tensors [pages, page_size, heads, dim] of any strides with
 adjacent row elements (a transposed [pages, heads, page_size, dim] tensor too).
+There is no backward pass: while gradients are recorded, tensors that require
+them are refused.
 """
 from __future__ import annotations
 
@@ -146,6 +148,13 @@ def _cache(k_cache, v_cache):
     return KVCache(k_cache.data_ptr(), v, *shape, a[0], a[1], a[2], b[0], b[1], b[2])
 
 
+def _no_gradients(*tensors):
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            raise ValueError("the cache's calls have no backward pass, and a tensor requires gradients: call them under "
+                             "torch.no_grad()")
+
+
 def _table(t, index: int):
     if t.dtype is not torch.int32 or t.dim() != 2 or t.get_device() != index:
         raise ValueError(f"block_table must be an int32 matrix on cuda:{index}")
@@ -202,6 +211,8 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_ca
     ``positions`` the rotation.  Token t goes to slot ``slots[t]`` (None: slot t; out of range: padding).  Returns
     the queries (``out``, or a new tensor; ``out`` may be q).
     """
+    if torch.is_grad_enabled():
+        _no_gradients(q, k, v, k_cache, v_cache, q_weight, k_weight, rope, out)
     cache = _cache(k_cache, v_cache if v is not None else None)
     dev, dt = k_cache.get_device(), k_cache.dtype
     T, heads, dim = k.shape[0], cache.heads, cache.dim
@@ -254,6 +265,8 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     graph captures share nothing.  A ``ws`` serves one stream of calls at a time; graphs that captured it have to be
     gone before it is.
     """
+    if torch.is_grad_enabled():
+        _no_gradients(q, k_cache, v_cache, log_weight, out, lse if isinstance(lse, torch.Tensor) else None)
     cache = _cache(k_cache, v_cache)
     dev, dt = k_cache.get_device(), k_cache.dtype
     T, hq = q.shape[0], q.shape[1]

@@ -52,3 +52,25 @@ def test_scale_that_overflows_in_units_of_log_2():
     assert _attend(L, scale=3e38) == 1 and "scale" in _said(L)
     assert _attend(L, scale=-3e38) == 1
     assert _attend(L, scale=3e38, lw=FAKE, ws=None, nb=0) == 3  # (with weights they are natural: only the workspace lacks)
+
+
+def test_tensors_that_require_gradients_are_refused():
+    """There is no backward pass, so results would have no history."""
+    c = torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16)
+    x, w = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.zeros(64)
+    i = torch.zeros(1, dtype=torch.int32)
+    g = lambda t: t.clone().requires_grad_()
+    for kw in (dict(q=g(x)), dict(k=g(x)), dict(v=g(x)), dict(k_cache=g(c)), dict(v_cache=g(c)), dict(q_weight=g(w)),
+               dict(k_weight=g(w)), dict(rope=g(w)), dict(out=g(x))):
+        a = dict(dict(q=x, k=x, v=x, k_cache=c, v_cache=c, slots=None), **kw)
+        with pytest.raises(ValueError, match="no backward"):
+            kvcache.append(**a)
+        with torch.no_grad(), pytest.raises(ValueError, match="device"):  # (the next check: host tensors)
+            kvcache.append(**a)
+    for kw in (dict(q=g(x)), dict(k_cache=g(c)), dict(v_cache=g(c)), dict(log_weight=g(w)), dict(out=g(x)),
+               dict(lse=g(w))):
+        a = dict(dict(q=x, k_cache=c, v_cache=c, block_table=i[None], query_start=i, seq_lens=i), **kw)
+        with pytest.raises(ValueError, match="no backward"):
+            kvcache.attend(**a)
+        with torch.inference_mode(), pytest.raises(ValueError, match="device"):
+            kvcache.attend(**a)
