@@ -33,6 +33,7 @@ class Server:
         self.table = torch.full((1, pages), -1, dtype=torch.int32, device=device)
         self.held = torch.zeros(1, dtype=torch.int32, device=device)    # slots in the cache
         self.offset = torch.zeros(1, dtype=torch.int32, device=device)  # tokens seen but not held
+        self.centroids = 0  # leading slots that hold centroids
         angle = torch.arange(max_pos, device=device)[:, None] * torch.pow(
             10000.0, -torch.arange(0, dim, 2, device=device) / dim)[None]
         self.rope = torch.cat([angle.cos(), angle.sin()], dim=1)
@@ -53,19 +54,25 @@ class Server:
         return out
 
     def compress(self, slots, clusters, iters=8):
-        """Replaces the request's first `slots` slots (whole pages of tokens) by `clusters` centroids (whole pages)."""
+        """Replaces the request's oldest `slots` tokens (whole pages) by `clusters` centroids (whole pages).
+
+        The centroids of earlier calls stay as they are: K-Means would count each of them as one key.
+        """
         p, h, d = self.page_size, self.heads, self.dim
-        if slots % p or clusters % p or clusters > slots:
-            raise ValueError("slots and clusters must be whole pages, and the clusters fewer")
-        old = self.table[0, :slots // p].clone()
+        if slots % p or clusters % p or not 0 < clusters <= slots:
+            raise ValueError("slots and clusters must be whole pages, and not more clusters than slots")
+        first, last = self.centroids // p, (self.centroids + slots) // p
+        if last * p > int(self.held):
+            raise ValueError(f"the cache holds {int(self.held) - self.centroids} tokens, fewer than {slots}")
+        old = self.table[0, first:last].clone()
         keys = self.k[old.long()].view(slots, h, d).transpose(0, 1).contiguous()
         values = self.v[old.long()].view(slots, h, d).transpose(0, 1).reshape(h * slots, d)
         # centroids start at keys spread over the context
-        first = keys[:, torch.arange(clusters, device=keys.device) * slots // clusters].float().contiguous()
-        centroids, assign, counts, _ = km.fit_batched(keys, first, iters)
+        spread = keys[:, torch.arange(clusters, device=keys.device) * slots // clusters].float().contiguous()
+        centroids, assign, counts, _ = km.fit_batched(keys, spread, iters)
         cluster = assign + torch.arange(h, dtype=torch.int32, device=keys.device)[:, None] * clusters
         means, _ = km.update(values, cluster.view(-1), torch.zeros(h * clusters, d, device=keys.device))
-        # the centroids go into the first of the old pages, the others are free again
+        # the centroids go into the first of the old pages, the others (whose weights are a token's, 0) are free again
         kept = old[:clusters // p]
         at = torch.arange(clusters, dtype=torch.int32, device=keys.device)
         kvcache.append(None, centroids.transpose(0, 1).to(keys.dtype).contiguous(),
@@ -74,7 +81,9 @@ class Server:
         # (-inf where a cluster is empty)
         self.log_weight[kept.long()] = counts.view(h, clusters // p, p).transpose(0, 1).float().log()
         self.free = torch.cat([old[clusters // p:], self.free])
-        self.table = torch.cat([kept, self.table[0, slots // p:], old.new_full(((slots - clusters) // p,), -1)])[None]
+        self.table = torch.cat([self.table[0, :first], kept, self.table[0, last:],
+                                old.new_full(((slots - clusters) // p,), -1)])[None]
+        self.centroids += clusters
         self.held = self.held - (slots - clusters)
         self.offset = self.offset + (slots - clusters)
 
