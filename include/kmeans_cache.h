@@ -104,7 +104,7 @@ km_status kmeans_kv_tables(const int32_t* ctx_lens, const int32_t* new_lens, con
  * A token whose slot is not in the cache or whose position is not in
  * [0, max_pos) is padding: its q_out row is zero and the cache is not written.
  * No two tokens of a call may share a slot.
- * Limits: T * (q_heads + 2 * heads) <= 2^28 (beyond: KM_ERR_UNSUPPORTED).
+ * Limits: T * (q_heads + 2 * heads) <= 2^28 - 16 (beyond: KM_ERR_UNSUPPORTED).
  */
 km_status kmeans_kv_append(const km_kv_cache* cache, km_dtype dt, int64_t T, const void* q, int64_t q_heads,
                            int64_t q_token, int64_t q_head, const void* k, int64_t k_token, int64_t k_head,

@@ -28,9 +28,9 @@ km_status launched(hipError_t e) noexcept {
 bool aligned(const void* p, size_t a) { return (uintptr_t)p % a == 0; }
 constexpr int64_t kMaxI = ((int64_t)1 << 31) - 1, kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxRoom = (int64_t)1 << 30;  // slots of a row of the block table
-// A launch has fewer than 2^32 threads: 16 for a row of the append, 256 for
-// an item or a token of the attention.
-constexpr int64_t kMaxRows = (int64_t)1 << 28, kMaxGroups = ((int64_t)1 << 24) - 1;
+// A launch has fewer than 2^32 threads: workgroups of 256, which take at least
+// 16 rows of the append, or an item or a token of the attention.
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1, kMaxRows = 16 * kMaxGroups;
 
 int shift_of(int64_t page_size) {
   int s = 0;
@@ -177,7 +177,7 @@ extern "C" km_status kmeans_kv_append(const km_kv_cache* cache, km_dtype dt, int
   if (q_heads < 0 || q_heads > (1 << 20)) return invalid("q_heads must be 0 to 2^20");
   if (T < 0 || T > kMaxI) return invalid("T must be 0 to 2^31 - 1");
   if (T * (q_heads + 2 * cache->heads) > kMaxRows)
-    return fail(KM_ERR_UNSUPPORTED, "T * (q_heads + 2 * heads) must be at most 2^28");
+    return fail(KM_ERR_UNSUPPORTED, "T * (q_heads + 2 * heads) must be at most 2^28 - 16");
   if (!(eps >= 0.f)) return invalid("eps must not be negative");
   if (rot < 0 || rot > cache->dim || rot % 16) return invalid("rot must be a multiple of 16 up to the cache's dim");
   if (rot > 0 && (!rope || !positions || max_pos < 1 || max_pos > kMaxI))

@@ -6,7 +6,7 @@ import torch
 
 from means_clustering_amd import kvcache
 
-from .test_kvcache_abi import FAKE, _attend, _said
+from .test_kvcache_abi import FAKE, _append, _attend, _cache, _said
 
 HOST = -1  # the device index of host tensors
 
@@ -74,3 +74,10 @@ def test_tensors_that_require_gradients_are_refused():
             kvcache.attend(**a)
         with torch.inference_mode(), pytest.raises(ValueError, match="device"):
             kvcache.attend(**a)
+
+
+def test_append_of_more_rows_than_a_launch_has():
+    """Rows of more than 128 elements take 16 threads each: 2^28 of them would be a launch of 2^32 threads."""
+    L = kvcache.lib()
+    wide = _cache(dim=256, heads=1)
+    assert _append(L, wide, T=1 << 26, hq=2) == 2 and "2^28 - 16" in _said(L)
