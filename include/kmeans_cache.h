@@ -149,7 +149,7 @@ size_t kmeans_kv_attend_workspace(const km_kv_cache* cache, int64_t T, int64_t q
  * below 2^-28 and none below 2^-39 of the row's largest so far.  (So a visible
  * infinite value whose term is 0 can make its row NaN.)  Results do not depend
  * on scheduling.
- * Limits: q_heads a multiple of heads; T, R < 2^24; T * q_heads < 2^31; width *
+ * Limits: q_heads a multiple of heads up to 2^17; T, R < 2^24; T * q_heads < 2^31; width *
  * page_size <= 2^30; (R + T * q_heads / heads / 128) * heads below about 2^24
  * (beyond: KM_ERR_UNSUPPORTED).
  */

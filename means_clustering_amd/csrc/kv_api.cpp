@@ -116,7 +116,8 @@ Plan make_plan(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t R, int64_t
 const char* attend_error(const km_kv_cache* c, int64_t T, int64_t Hq, int64_t R, int64_t max_new) {
   if (const char* e = cache_error(c, true)) return e;
   if (T < 0 || T > kMaxGroups || R < 0 || R > kMaxGroups) return "T and R must be 0 to 2^24 - 1";
-  if (Hq < 1 || Hq % c->heads || Hq > (1 << 20)) return "q_heads must be a multiple of the cache's heads";
+  // (the join has a workgroup row for every 4 query heads or more, and a launch 65,535 of them)
+  if (Hq < 1 || Hq % c->heads || Hq > (1 << 17)) return "q_heads must be a multiple of the cache's heads up to 2^17";
   if (T * Hq > kMaxI) return "T * q_heads must be below 2^31";
   if (max_new < 0 || max_new > kMaxI) return "max_new must be 0 to 2^31 - 1";
   return nullptr;

@@ -81,3 +81,11 @@ def test_append_of_more_rows_than_a_launch_has():
     L = kvcache.lib()
     wide = _cache(dim=256, heads=1)
     assert _append(L, wide, T=1 << 26, hq=2) == 2 and "2^28 - 16" in _said(L)
+
+
+def test_attend_of_more_query_heads_than_the_join_takes():
+    L = kvcache.lib()
+    wide = _cache(dim=256, heads=2)
+    assert _attend(L, wide, hq=1 << 18) == 1 and "2^17" in _said(L)
+    assert L.kmeans_kv_attend_workspace(wide, 4, 1 << 18, 2, 4) == 0
+    assert L.kmeans_kv_attend_workspace(wide, 4, 1 << 17, 2, 4) > 0
