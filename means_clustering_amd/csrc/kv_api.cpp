@@ -146,6 +146,12 @@ extern "C" km_status kmeans_kv_tables(const int32_t* ctx_lens, const int32_t* ne
                         (const void*)query_start, (const void*)page_start, (const void*)positions,
                         (const void*)slots})
     if (!aligned(p, 4)) return invalid("pointers must be 4-byte aligned");
+  // the workgroups read the lengths for themselves, at different times
+  for (const void* out : {(const void*)seq_lens, (const void*)query_start, (const void*)page_start,
+                          (const void*)positions, (const void*)slots})
+    for (const void* in : {(const void*)ctx_lens, (const void*)new_lens, (const void*)pos_offset,
+                           (const void*)free_pages})
+      if (R > 0 && out && out == in) return invalid("an output must not be an input");
   TablesArgs a;
   a.ctx = ctx_lens;
   a.fresh = new_lens;

@@ -6,7 +6,7 @@ import torch
 
 from means_clustering_amd import kvcache
 
-from .test_kvcache_abi import FAKE, _append, _attend, _cache, _said
+from .test_kvcache_abi import FAKE, _append, _attend, _cache, _said, _tables
 
 HOST = -1  # the device index of host tensors
 
@@ -89,3 +89,13 @@ def test_attend_of_more_query_heads_than_the_join_takes():
     assert _attend(L, wide, hq=1 << 18) == 1 and "2^17" in _said(L)
     assert L.kmeans_kv_attend_workspace(wide, 4, 1 << 18, 2, 4) == 0
     assert L.kmeans_kv_attend_workspace(wide, 4, 1 << 17, 2, 4) > 0
+
+
+def test_tables_in_place_are_refused():
+    """Lengths that are updated while other workgroups still read them would be a race."""
+    L = kvcache.lib()
+    free = dict(ctx=FAKE, new=FAKE + 256, off=FAKE + 512, free=FAKE + 768, seq=FAKE + 1024, qs=FAKE + 1280, ps=FAKE + 1536,
+                pos=FAKE + 1792, slots=FAKE + 2048)
+    for out in ("seq", "qs", "ps", "pos", "slots"):
+        for given in ("ctx", "new", "off", "free"):
+            assert _tables(L, **dict(free, **{out: free[given]})) == 1 and "must not be an input" in _said(L)
