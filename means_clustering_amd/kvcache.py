@@ -171,6 +171,16 @@ def _table(t, index: int):
 
 # The handle of a device's current stream (torch.cuda.current_stream would make a Stream object of it).
 _stream = torch._C._cuda_getCurrentRawStream
+_device = torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+
+
+def _launch(dev: int, fn, *args) -> int:
+    """fn(*args) with the tensors' device as the current one, to whose streams a launch belongs."""
+    if _device() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -193,9 +203,9 @@ def tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Te
     # one allocation, five views: seq_lens, query_start, page_start, positions, slots
     seq, qs, ps, pos, slots = ctx_lens.new_empty(3 * R + 2 + 2 * total).split_with_sizes(
         (R, R + 1, R + 1, total, total))
-    _check(lib().kmeans_kv_tables(c, n, o, R, page_size, block_table.data_ptr(), width, stride, f,
-                                  free_pages.shape[0], total, seq.data_ptr(), qs.data_ptr(), ps.data_ptr(),
-                                  pos.data_ptr(), slots.data_ptr(), _stream(dev)))
+    _check(_launch(dev, lib().kmeans_kv_tables, c, n, o, R, page_size, block_table.data_ptr(), width, stride, f,
+                   free_pages.shape[0], total, seq.data_ptr(), qs.data_ptr(), ps.data_ptr(), pos.data_ptr(),
+                   slots.data_ptr(), _stream(dev)))
     return Tables(seq, qs, ps, pos, slots)
 
 
@@ -241,10 +251,9 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_ca
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None:
             _floats(w, name, dev, (dim,))
-    _check(lib().kmeans_kv_append(cache, _DT[dt], T, _ptr(q), hq, qs[0], qs[1], k.data_ptr(), ks[0], ks[1], _ptr(v),
-                                  vs[0], vs[1], _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), _ptr(rope),
-                                  max_pos, rot, bool(interleaved), _ptr(slots), _ptr(out) if hq else None, os_[0],
-                                  os_[1], _stream(dev)))
+    _check(_launch(dev, lib().kmeans_kv_append, cache, _DT[dt], T, _ptr(q), hq, qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+                   _ptr(v), vs[0], vs[1], _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), _ptr(rope), max_pos, rot,
+                   bool(interleaved), _ptr(slots), _ptr(out) if hq else None, os_[0], os_[1], _stream(dev)))
     return out
 
 
@@ -296,13 +305,13 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
         buf = q.new_empty(L.kmeans_kv_attend_workspace(cache, T, hq, R, max_new), dtype=torch.uint8)
     else:
         buf = ws.buf if ws.buf is not None and ws.buf.get_device() == dev else None
-        if buf is not None and torch.cuda.is_current_stream_capturing():
+        if buf is not None and _capturing():
             ws.hold()
     for _ in range(2):
-        status = L.kmeans_kv_attend(cache, _DT[dt], q.data_ptr(), T, hq, qs[0], qs[1], block_table.data_ptr(), R, width,
-                                    tstride, starts, lens, _ptr(log_weight), lw_page, lw_head,
-                                    cache.dim ** -0.5 if scale is None else scale, window, max_new, out.data_ptr(),
-                                    os_[0], os_[1], l, _ptr(buf), 0 if buf is None else buf.numel(), stream)
+        status = _launch(dev, L.kmeans_kv_attend, cache, _DT[dt], q.data_ptr(), T, hq, qs[0], qs[1],
+                         block_table.data_ptr(), R, width, tstride, starts, lens, _ptr(log_weight), lw_page, lw_head,
+                         cache.dim ** -0.5 if scale is None else scale, window, max_new, out.data_ptr(), os_[0], os_[1],
+                         l, _ptr(buf), 0 if buf is None else buf.numel(), stream)
         if status != KM_ERR_WORKSPACE or ws is None:
             break
         # the first call, or a larger one than before (the workspace is the last argument to be refused)

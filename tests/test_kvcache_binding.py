@@ -99,3 +99,24 @@ def test_tables_in_place_are_refused():
     for out in ("seq", "qs", "ps", "pos", "slots"):
         for given in ("ctx", "new", "off", "free"):
             assert _tables(L, **dict(free, **{out: free[given]})) == 1 and "must not be an input" in _said(L)
+
+
+def test_launches_go_to_the_device_of_the_tensors(monkeypatch):
+    """A stream handle of 0 is the default stream of whichever device is current."""
+    current = [0]
+
+    class device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.d
+
+        def __exit__(self, *e):
+            current[0] = self.before
+
+    monkeypatch.setattr(kvcache, "_device", lambda: current[0])
+    monkeypatch.setattr(kvcache.torch.cuda, "device", device)
+    assert kvcache._launch(1, lambda x: (x, current[0]), 7) == (7, 1)
+    assert kvcache._launch(0, lambda x: (x, current[0]), 8) == (8, 0)
+    assert current == [0]
