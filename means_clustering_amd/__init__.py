@@ -132,6 +132,9 @@ class Workspace:
     def get(self, nbytes: int, device) -> torch.Tensor:
         nbytes = max(int(nbytes), 256)
         if self.buf is None or self.buf.numel() < nbytes or self.buf.device != torch.device(device):
+            if self.buf is not None and self.buf.is_cuda:
+                # calls on this stream may still use it, whichever stream it was allocated on
+                self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
             self.buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
         if self.buf.is_cuda and torch.cuda.is_current_stream_capturing():
             self.hold()

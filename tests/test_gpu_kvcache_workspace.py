@@ -157,3 +157,23 @@ def test_graph_with_a_workspace_that_grows_later():
         assert torch.equal(kvcache.attend(**large, ws=ws), want_large)
         torch.cuda.synchronize()
         assert all(bool((f == 7).all()) for f in filled)
+
+
+def test_buffer_replaced_on_another_stream_is_not_reused_at_once():
+    """A workspace allocated on one stream and outgrown on another: work in flight on that one still has the buffer."""
+    n = 3 << 20
+    ws = kvcache.Workspace(DEV)
+    first = ws.get(n, DEV).data_ptr()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(100_000_000)
+        ws.buf.zero_()
+        ws.get(2 * n, DEV)
+        busy = not s.query()
+    again = torch.empty(n, dtype=torch.uint8, device=DEV)
+    still = busy and not s.query()
+    s.synchronize()
+    if not still:
+        pytest.skip("the stream was done too early to tell")
+    assert again.data_ptr() != first
