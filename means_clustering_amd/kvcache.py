@@ -148,11 +148,9 @@ def _cache(k_cache, v_cache):
     return KVCache(k_cache.data_ptr(), v, *shape, a[0], a[1], a[2], b[0], b[1], b[2])
 
 
-def _no_gradients(*tensors):
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            raise ValueError("the cache's calls have no backward pass, and a tensor requires gradients: call them under "
-                             "torch.no_grad()")
+def _no_backward():
+    raise ValueError("the cache's calls have no backward pass, and a tensor requires gradients: call them under "
+                     "torch.no_grad()")
 
 
 def _table(t, index: int):
@@ -173,14 +171,18 @@ def _table(t, index: int):
 _stream = torch._C._cuda_getCurrentRawStream
 _device = torch._C._cuda_getDevice
 _capturing = torch._C._cuda_isCurrentStreamCapturing
+_recording = torch.is_grad_enabled
 
 
-def _launch(dev: int, fn, *args) -> int:
-    """fn(*args) with the tensors' device as the current one, to whose streams a launch belongs."""
+def _on(dev: int, fn):
+    """fn with the tensors' device as the current one, to whose streams a launch belongs."""
     if _device() == dev:
-        return fn(*args)
-    with torch.cuda.device(dev):
-        return fn(*args)
+        return fn
+
+    def there(*args):
+        with torch.cuda.device(dev):
+            return fn(*args)
+    return there
 
 
 def tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -203,9 +205,9 @@ def tables(ctx_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Te
     # one allocation, five views: seq_lens, query_start, page_start, positions, slots
     seq, qs, ps, pos, slots = ctx_lens.new_empty(3 * R + 2 + 2 * total).split_with_sizes(
         (R, R + 1, R + 1, total, total))
-    _check(_launch(dev, lib().kmeans_kv_tables, c, n, o, R, page_size, block_table.data_ptr(), width, stride, f,
-                   free_pages.shape[0], total, seq.data_ptr(), qs.data_ptr(), ps.data_ptr(), pos.data_ptr(),
-                   slots.data_ptr(), _stream(dev)))
+    _check(_on(dev, lib().kmeans_kv_tables)(
+        c, n, o, R, page_size, block_table.data_ptr(), width, stride, f, free_pages.shape[0], total, seq.data_ptr(),
+        qs.data_ptr(), ps.data_ptr(), pos.data_ptr(), slots.data_ptr(), _stream(dev)))
     return Tables(seq, qs, ps, pos, slots)
 
 
@@ -221,8 +223,10 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_ca
     ``positions`` the rotation.  Token t goes to slot ``slots[t]`` (None: slot t; out of range: padding).  Returns
     the queries (``out``, or a new tensor; ``out`` may be q).
     """
-    if torch.is_grad_enabled():
-        _no_gradients(q, k, v, k_cache, v_cache, q_weight, k_weight, rope, out)
+    if _recording():
+        for t in (q, k, v, k_cache, v_cache, q_weight, k_weight, rope, out):
+            if t is not None and t.requires_grad:
+                _no_backward()
     cache = _cache(k_cache, v_cache if v is not None else None)
     dev, dt = k_cache.get_device(), k_cache.dtype
     T, heads, dim = k.shape[0], cache.heads, cache.dim
@@ -240,20 +244,23 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_ca
     if (rope is None) != (positions is None):
         raise ValueError("rope and positions go together")
     max_pos = rot = 0
+    rope_at = pos_at = slots_at = qw_at = kw_at = None
     if rope is not None:
         if rope.dim() != 2:
             raise ValueError("rope must be [max_pos, rot]")
         max_pos, rot = rope.shape
-        _floats(rope, "rope", dev, (max_pos, rot))
-        _ints(positions, "positions", dev, T)
+        rope_at = _floats(rope, "rope", dev, (max_pos, rot))
+        pos_at = _ints(positions, "positions", dev, T)
     if slots is not None:
-        _ints(slots, "slots", dev, T)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _floats(w, name, dev, (dim,))
-    _check(_launch(dev, lib().kmeans_kv_append, cache, _DT[dt], T, _ptr(q), hq, qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
-                   _ptr(v), vs[0], vs[1], _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), _ptr(rope), max_pos, rot,
-                   bool(interleaved), _ptr(slots), _ptr(out) if hq else None, os_[0], os_[1], _stream(dev)))
+        slots_at = _ints(slots, "slots", dev, T)
+    if q_weight is not None:
+        qw_at = _floats(q_weight, "q_weight", dev, (dim,))
+    if k_weight is not None:
+        kw_at = _floats(k_weight, "k_weight", dev, (dim,))
+    _check(_on(dev, lib().kmeans_kv_append)(
+        cache, _DT[dt], T, _ptr(q), hq, qs[0], qs[1], k.data_ptr(), ks[0], ks[1], _ptr(v), vs[0], vs[1], qw_at, kw_at, eps,
+        pos_at, rope_at, max_pos, rot, bool(interleaved), slots_at, _ptr(out) if hq else None, os_[0], os_[1],
+        _stream(dev)))
     return out
 
 
@@ -274,15 +281,18 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     graph captures share nothing.  A ``ws`` serves one stream of calls at a time; graphs that captured it have to be
     gone before it is.
     """
-    if torch.is_grad_enabled():
-        _no_gradients(q, k_cache, v_cache, log_weight, out, lse if isinstance(lse, torch.Tensor) else None)
+    if _recording() and (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad or (
+            out is not None and out.requires_grad) or (log_weight is not None and log_weight.requires_grad) or (
+            lse is not True and lse is not False and lse.requires_grad)):
+        _no_backward()
     cache = _cache(k_cache, v_cache)
-    dev, dt = k_cache.get_device(), k_cache.dtype
-    T, hq = q.shape[0], q.shape[1]
-    qs = _rows(q, "q", dev, dt, (T, hq, cache.dim))
+    dev, dt, dim = k_cache.get_device(), k_cache.dtype, cache.dim
+    shape = q.shape
+    T, hq = shape[0], shape[1]
+    qs = _rows(q, "q", dev, dt, (T, hq, dim))
     if out is None:
-        out = q.new_empty((T, hq, cache.dim))
-    os_ = _rows(out, "out", dev, dt, (T, hq, cache.dim))
+        out = q.new_empty((T, hq, dim))
+    os_ = _rows(out, "out", dev, dt, (T, hq, dim))
     R, width, tstride = _table(block_table, dev)
     starts, lens = _ints(query_start, "query_start", dev, R + 1), _ints(seq_lens, "seq_lens", dev, R)
     lw_page = lw_head = 0
@@ -304,14 +314,17 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
         # (freed at the end: the allocator gives it to later work of this stream only, a graph's stays the graph's)
         buf = q.new_empty(L.kmeans_kv_attend_workspace(cache, T, hq, R, max_new), dtype=torch.uint8)
     else:
-        buf = ws.buf if ws.buf is not None and ws.buf.get_device() == dev else None
-        if buf is not None and _capturing():
-            ws.hold()
+        buf = ws.buf
+        if buf is not None:
+            if buf.get_device() != dev:
+                buf = None
+            elif _capturing():
+                ws.hold()
     for _ in range(2):
-        status = _launch(dev, L.kmeans_kv_attend, cache, _DT[dt], q.data_ptr(), T, hq, qs[0], qs[1],
-                         block_table.data_ptr(), R, width, tstride, starts, lens, _ptr(log_weight), lw_page, lw_head,
-                         cache.dim ** -0.5 if scale is None else scale, window, max_new, out.data_ptr(), os_[0], os_[1],
-                         l, _ptr(buf), 0 if buf is None else buf.numel(), stream)
+        status = _on(dev, L.kmeans_kv_attend)(
+            cache, _DT[dt], q.data_ptr(), T, hq, qs[0], qs[1], block_table.data_ptr(), R, width, tstride, starts, lens,
+            _ptr(log_weight), lw_page, lw_head, dim ** -0.5 if scale is None else scale, window, max_new,
+            out.data_ptr(), os_[0], os_[1], l, _ptr(buf), 0 if buf is None else buf.numel(), stream)
         if status != KM_ERR_WORKSPACE or ws is None:
             break
         # the first call, or a larger one than before (the workspace is the last argument to be refused)

@@ -117,6 +117,6 @@ def test_launches_go_to_the_device_of_the_tensors(monkeypatch):
 
     monkeypatch.setattr(kvcache, "_device", lambda: current[0])
     monkeypatch.setattr(kvcache.torch.cuda, "device", device)
-    assert kvcache._launch(1, lambda x: (x, current[0]), 7) == (7, 1)
-    assert kvcache._launch(0, lambda x: (x, current[0]), 8) == (8, 0)
+    assert kvcache._on(1, lambda x: (x, current[0]))(7) == (7, 1)
+    assert kvcache._on(0, lambda x: (x, current[0]))(8) == (8, 0)
     assert current == [0]
