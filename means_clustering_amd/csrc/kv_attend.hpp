@@ -195,39 +195,44 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int it, Item& out
   __syncthreads();
   const float total = (costs[0] + costs[1]) + (costs[2] + costs[3]);
   const int size = max((int)fminf(total * 1.0001f / (float)a.target, 1e9f) + 1, a.min_units);
-  auto count = [&](const Request& q, int& items, int& parts) {
+  // (A launch has fewer than 2^24 items; requests that overlap, an error of the caller, could have any number, so each
+  // thread's count ends there and the sums stay below 2^32: an item belongs to one thread only.)
+  constexpr unsigned kMost = (1u << 24) - 1;
+  auto count = [&](const Request& q, unsigned& items, unsigned& parts) {
     const int splits = (q.units + size - 1) / size;
-    items = q.tiles * splits;
-    parts = splits > 1 ? items : 0;
+    const uint64_t n = (uint64_t)q.tiles * (unsigned)splits;
+    items = n < kMost ? (unsigned)n : kMost;
+    parts = splits > 1 ? items : 0u;
   };
-  int items, parts;
+  unsigned items, parts;
   count(q0, items, parts);
   for (int r = r0 + 1; r < r1; ++r) {
-    int i, p;
+    unsigned i, p;
     count(request_of<BM, UNIT>(a, r), i, p);
-    items += i;
-    parts += p;
+    items = min(items + i, kMost);
+    parts = min(parts + p, kMost);
   }
-  int last = wave_scan(items), plast = wave_scan(parts);
+  unsigned last = wave_scan(items), plast = wave_scan(parts);
   if (lane == 63) {
-    scratch[4 + wave] = last;
-    scratch[8 + wave] = plast;
+    scratch[4 + wave] = (int)last;
+    scratch[8 + wave] = (int)plast;
   }
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWgThreads / 64 - 1; ++w)
     if (w < wave) {
-      last += scratch[4 + w];
-      plast += scratch[8 + w];
+      last += (unsigned)scratch[4 + w];
+      plast += (unsigned)scratch[8 + w];
     }
-  int first = last - items, pfirst = plast - parts;
-  if (it >= first && it < last) {  // this thread's requests hold the item
+  unsigned first = last - items, pfirst = plast - parts;
+  const unsigned at = (unsigned)it;
+  if (at >= first && at < last) {  // this thread's requests hold the item
     for (int r = r0; r < r1; ++r) {
       const Request q = r == r0 ? q0 : request_of<BM, UNIT>(a, r);
-      int i, p;
+      unsigned i, p;
       count(q, i, p);
-      if (it < first + i) {
-        const int v[9] = {r, it - first, pfirst, q.q0, q.n, q.seq, q.c, q.tiles, q.units};
+      if (at - first < i) {
+        const int v[9] = {r, (int)(at - first), (int)pfirst, q.q0, q.n, q.seq, q.c, q.tiles, q.units};
 #pragma unroll
         for (int j = 0; j < 9; ++j) scratch[16 + j] = v[j];
         break;

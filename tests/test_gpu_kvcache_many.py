@@ -3,8 +3,11 @@ idle requests and into the next head, parts numbered across divided and whole re
 import random
 
 import pytest
+import torch
 
-from .test_gpu_kvcache import BF, FP, Case
+from means_clustering_amd import kvcache
+
+from .test_gpu_kvcache import BF, DEV, FP, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +68,19 @@ def test_one_busy_request_among_many():
     lens = [(0, 0)] * 900
     lens[77], lens[640] = (700, 1), (1500, 60)
     Case(lens, 4, 2, 64, BF).check()
+
+
+def test_overlapping_requests_with_more_tiles_than_32_bits_count():
+    """33,000 requests that all claim the same 2^19 tokens (an error of the caller): 2^31 tiles and more.  The call
+    stays inside every buffer, and later calls are right."""
+    T, n = 1 << 19, 33000
+    q = torch.zeros(T, 16, 16, dtype=BF, device=DEV)
+    k = torch.zeros(1, 16, 1, 16, dtype=BF, device=DEV)
+    starts = torch.zeros(2 * n + 1, dtype=torch.int32)
+    starts[1::2] = T
+    out = torch.zeros_like(q)
+    kvcache.attend(q, k, k, torch.zeros(2 * n, 1, dtype=torch.int32, device=DEV), starts.to(DEV),
+                   torch.full((2 * n,), 16, dtype=torch.int32, device=DEV), out=out)
+    torch.cuda.synchronize()
+    assert bool((out == 0).all())  # (values of zero)
+    Case([(300, 40), (200, 1)], 4, 2, 64, BF).check()
