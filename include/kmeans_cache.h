@@ -40,8 +40,8 @@ extern "C" {
  * head are free (pages x slots x heads x dim and pages x heads x slots x dim
  * are both usual), elements of a row are adjacent.  Rows must be 16-byte
  * aligned: k and v 16-byte aligned, strides multiples of 8.
- * Limits: dim a multiple of 16 up to 256; page_size a power of two of at
- * least 16; pages * page_size < 2^31; strides < 2^40.
+ * Limits: dim a multiple of 16 up to 256; heads up to 65,536; page_size a power
+ * of two from 16 to 2^20; pages * page_size < 2^31; strides < 2^40.
  */
 typedef struct km_kv_cache {
   void* k;
@@ -74,8 +74,9 @@ typedef struct km_kv_cache {
  * position 0 and slot -1; tokens that find no room (free list or table row
  * exhausted: page_start[R] > num_free, or need > width) get slot -1 and their
  * table entries -1.  Tokens in a page that no cache can have (negative, or
- * 2^31 / page_size or more) get slot -1.  Sums of lengths must stay below 2^31.  Limits: R < 2^24;
- * width * page_size < 2^31.
+ * 2^31 / page_size or more) get slot -1.  Outputs overlap neither each other nor
+ * inputs (ctx_lens is not updated in place).  Sums of lengths must stay below
+ * 2^31.  Limits: R < 2^24; width * page_size < 2^31.
  */
 km_status kmeans_kv_tables(const int32_t* ctx_lens, const int32_t* new_lens, const int32_t* pos_offset, int64_t R,
                            int64_t page_size, int32_t* block_table, int64_t width, int64_t table_stride,
@@ -104,7 +105,8 @@ km_status kmeans_kv_tables(const int32_t* ctx_lens, const int32_t* new_lens, con
  * A token whose slot is not in the cache or whose position is not in
  * [0, max_pos) is padding: its q_out row is zero and the cache is not written.
  * No two tokens of a call may share a slot.
- * Limits: T * (q_heads + 2 * heads) <= 2^28 - 16 (beyond: KM_ERR_UNSUPPORTED).
+ * Limits: q_heads up to 2^20; T * (q_heads + 2 * heads) <= 2^28 - 16 (beyond:
+ * KM_ERR_UNSUPPORTED).
  */
 km_status kmeans_kv_append(const km_kv_cache* cache, km_dtype dt, int64_t T, const void* q, int64_t q_heads,
                            int64_t q_token, int64_t q_head, const void* k, int64_t k_token, int64_t k_head,
@@ -149,9 +151,9 @@ size_t kmeans_kv_attend_workspace(const km_kv_cache* cache, int64_t T, int64_t q
  * below 2^-28 and none below 2^-39 of the row's largest so far.  (So a visible
  * infinite value whose term is 0 can make its row NaN.)  Results do not depend
  * on scheduling.
- * Limits: q_heads a multiple of heads up to 2^17; T, R < 2^24; T * q_heads < 2^31; width *
- * page_size <= 2^30; (R + T * q_heads / heads / 128) * heads below about 2^24
- * (beyond: KM_ERR_UNSUPPORTED).
+ * Limits: q_heads a multiple of heads up to 2^17; T, R < 2^24; T * q_heads <
+ * 2^31; width * page_size <= 2^30; (R + T * q_heads / heads / 128) * heads below
+ * about 2^24 (beyond: KM_ERR_UNSUPPORTED).
  */
 km_status kmeans_kv_attend(const km_kv_cache* cache, km_dtype dt, const void* q, int64_t T, int64_t q_heads,
                            int64_t q_token, int64_t q_head, const int32_t* block_table, int64_t R, int64_t width,

@@ -229,14 +229,14 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_ca
                 _no_backward()
     cache = _cache(k_cache, v_cache if v is not None else None)
     dev, dt = k_cache.get_device(), k_cache.dtype
-    T, heads, dim = k.shape[0], cache.heads, cache.dim
+    T, heads, dim = k.shape[0] if k.dim() else 0, cache.heads, cache.dim
     ks = _rows(k, "k", dev, dt, (T, heads, dim))
     if v is not None and v_cache is None:
         raise ValueError("v needs a v_cache")
     vs = _rows(v, "v", dev, dt, (T, heads, dim)) if v is not None else (0, 0)
     hq, qs, os_ = 0, (0, 0), (0, 0)
     if q is not None:
-        hq = q.shape[1]
+        hq = q.shape[1] if q.dim() == 3 else 0
         qs = _rows(q, "q", dev, dt, (T, hq, dim))
         if out is None:
             out = k.new_empty((T, hq, dim))
@@ -283,12 +283,12 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     """
     if _recording() and (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad or (
             out is not None and out.requires_grad) or (log_weight is not None and log_weight.requires_grad) or (
-            lse is not True and lse is not False and lse.requires_grad)):
+            isinstance(lse, torch.Tensor) and lse.requires_grad)):
         _no_backward()
     cache = _cache(k_cache, v_cache)
     dev, dt, dim = k_cache.get_device(), k_cache.dtype, cache.dim
     shape = q.shape
-    T, hq = shape[0], shape[1]
+    T, hq = (shape[0], shape[1]) if len(shape) == 3 else (0, 0)  # (of another number of dimensions _rows refuses it)
     qs = _rows(q, "q", dev, dt, (T, hq, dim))
     if out is None:
         out = q.new_empty((T, hq, dim))

@@ -194,3 +194,23 @@ def test_attend_scale_of_zero_with_infinite_queries(n):
     out = kvcache.attend(**c.device())
     nan = torch.isnan(out)
     assert bool(nan[0, 1].all()) and int(nan.sum()) == 64
+
+
+# ----------------------------------------------------------------------------------------------------- binding ----
+
+def test_tensors_of_other_dimensions_are_refused():
+    d = Case([(50, 1)], 4, 2, 64, BF).device()
+    k = d["k_cache"][0, :1]
+    for bad in (d["q"][0], d["q"][0, 0], d["q"][0, 0, 0], d["q"][None]):
+        with pytest.raises(ValueError, match="q must be"):
+            kvcache.attend(**dict(d, q=bad))
+        with pytest.raises(ValueError, match="q must be"):
+            kvcache.append(bad, k, None, d["k_cache"], None, None)
+        with pytest.raises(ValueError, match="k must be"):
+            kvcache.append(None, bad, None, d["k_cache"], None, None)
+
+
+def test_attend_without_lse():
+    d = Case([(50, 1)], 4, 2, 64, BF).device()
+    want = kvcache.attend(**d)
+    assert torch.equal(kvcache.attend(**d, lse=None), want) and torch.equal(kvcache.attend(**d, lse=True)[0], want)
