@@ -11,8 +11,9 @@
 //
 // Memory bounds it: 16,384 tokens of 32 + 8 + 8 heads of 128 (403 MB, and a
 // table row of 512 bytes a token that its heads share) take 75.8 us, 5.4 TB/s,
-// where a large copy reaches 4.9; 5 tokens take 3.6 us, a launch and two
-// dependent loads.
+// where a large copy reaches 4.9; 5 tokens take 3.4 us, a launch and two
+// dependent loads.  Rows of 80, 112 and 240 leave 3, 1 and 1 of 8, 8 and 16
+// lanes idle and reach 3.9, 4.7 and 5.0 TB/s at such sizes.
 #include "kv_internal.hpp"
 
 namespace kmkv {

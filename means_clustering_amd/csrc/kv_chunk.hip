@@ -25,11 +25,12 @@
 // reads of V, 4 neighbouring pieces of 4 rows) meet no bank twice.
 //
 // Measured (MI355X, bf16, 32 + 8 heads of 128): 8,192 tokens over 32,768 slots
-// 3.77-3.88 ms, 990-1,020 TFLOP/s, where torch's matrix products reach 1,190
+// 3.75-3.80 ms, 1,010-1,030 TFLOP/s, where torch's matrix products reach 1,190
 // (8,192 square) to 1,362 (16,384 square); 509 tokens over 30,509 slots
-// 267-278 us, 910-945 TFLOP/s.  The matrix cores are busy 51% of the time at 1.9 GHz, the
-// vector units 45% (5.5 instructions for each of the 32 products of a tile and
-// wavefront, one of them an exponential, at a quarter of the others' rate).
+// 273-317 us, 800-925 TFLOP/s.  The matrix cores are busy 49% of the time at 2.0 GHz, the
+// vector units 47% (5.6 instructions for each of the 32 products of a tile and
+// wavefront, one of them an exponential, at a quarter of the others' rate): in
+// sum nearly all of it, so the two hardly overlap.
 //   * Tiles copied to LDS directly, pages by scalar loads: 4.09 ms; through
 //     registers 7.15 (they left none for reads ahead of the products).
 //   * LDS pieces permuted for 256 bytes a cycle: no bank conflicts; by 8 rows
@@ -39,8 +40,11 @@
 //   * Heaviest rows first: 1% here, 9% for 2 x 2,047 tokens of 32 + 32 heads.
 //   * Scores a tile ahead, beside the softmax: 5% fewer cycles, but a lower
 //     clock: 2% here, 4-11% slower for D = 64, D = 256 and with weights.
-//   * D = 256 keeps one workgroup a compute unit and tiles of 32 keys (486
-//     TFLOP/s; tiles of 64 keys 440).
+//   * D = 256 keeps one workgroup a compute unit and tiles of 32 keys (10%
+//     faster than of 64): 4,096 tokens over 28,672 slots 4.70 ms, 760 TFLOP/s.
+//   * Dims between 64, 128 and 256 multiply zeros in LDS: in the same case D =
+//     80 668 TFLOP/s of its own products, 96 785, 192 588.
+//   * fp16: terms times 2^14, 0.6% slower than without.
 #include <type_traits>
 
 #include "kv_attend.hpp"

@@ -22,9 +22,11 @@
 //
 // What bounds it, measured (MI355X; a plain read of 1 GB reaches 6.3 TB/s, a
 // copy 4.9): 64 requests of up to 8,191 slots with 8 heads of 128 read 847 MB
-// in 155 us (5.5 TB/s), two of 131,000 slots with weights 428 MB in 84 us
+// in 155 us (5.5 TB/s), two of 131,000 slots with weights 428 MB in 83 us
 // (5.1 TB/s), the join after them 5-6 us; a single request of 500 slots takes
-// 8 us, the latencies of its lengths, pages, keys and of the two launches.
+// 8 us, the latencies of its lengths, pages and keys, and the join 3-4 more.
+// 63 requests of 32 + 8 heads of 256 read 1.3 GB in 217 us (6.0 TB/s) without
+// registers for a step ahead; of 80 (as 128, padding not read) 404 MB in 98.
 //   * Equal pieces of one line of keys against items of equal size per
 //     request: 255 requests of D = 64 149 us against 180, 63 requests of 5 new
 //     tokens 176 against 195 (items leave the last round of workgroups short).

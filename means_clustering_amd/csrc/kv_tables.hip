@@ -11,8 +11,8 @@
 // dependent loads a token.  Up to 4,096 requests every workgroup makes the sums
 // itself in LDS, so that one launch does: 8 requests take 3.0 us, 250 with
 // 18,108 new tokens 4.7, 4,095 with 138,650 new tokens 10.8 (25 with the sums in
-// a launch of one workgroup before it, as above 4,096).  LDS arrays of 512 or
-// 4,096 requests.
+// a launch of one workgroup before it, as above 4,096: 9,001 take 27 + 9).  LDS
+// arrays of 512 or 4,096 requests.
 #include "kv_internal.hpp"
 
 namespace kmkv {

@@ -274,8 +274,8 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     slots; each sees the slots up to its own, with ``window`` > 0 only the last ``window`` of them.  ``log_weight``
     (fp32 [pages, heads, page_size]) is added to the scores: the logarithm of the number of keys that a centroid
     stands for, 0 for a token, -inf for none.  ``scale`` defaults to dim ** -0.5.  ``max_new`` bounds the new tokens
-    of any request (1 in a decode step).  ``lse`` True or an fp32 [T, q_heads] tensor also gives the logarithm of each
-    row's sum.  Returns out, or (out, lse).
+    of any request (1 in a decode step; left out, it is T, and the kernel for chunks is launched as well).  ``lse``
+    True or an fp32 [T, q_heads] tensor also gives the logarithm of each row's sum.  Returns out, or (out, lse).
 
     Without ``ws`` each call takes its workspace from torch's allocator, so calls of several threads and calls that a
     graph captures share nothing.  A ``ws`` serves one stream of calls at a time; graphs that captured it have to be
