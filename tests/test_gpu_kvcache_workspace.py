@@ -177,3 +177,28 @@ def test_buffer_replaced_on_another_stream_is_not_reused_at_once():
     if not still:
         pytest.skip("the stream was done too early to tell")
     assert again.data_ptr() != first
+
+
+def test_workspace_that_grows_inside_a_capture():
+    """A larger call captured with a workspace of an eager, smaller one, then eager calls of both sizes between replays."""
+    small, large = _inputs(SHAPES[0]), _inputs(SHAPES[2], seed=3)
+    ws = kvcache.Workspace(DEV)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        want_small = kvcache.attend(**small, ws=ws)
+        want, wl = kvcache.attend(**large, lse=True)
+    s.synchronize()
+    graph, (got, gl) = _capture(s, large, ws=ws)
+    filled = _fill()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got.zero_(), gl.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(gl, wl)
+        assert torch.equal(kvcache.attend(**small, ws=ws), want_small)
+        assert torch.equal(kvcache.attend(**large, ws=ws), want)
+        torch.cuda.synchronize()
+        assert all(bool((f == 7).all()) for f in filled)
