@@ -301,7 +301,8 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(At
         for (int i = 0; i < 16; ++i) o[d][i] *= al;
       m_ = mn;
     }
-    // the exponent of a term is score * factor + base; from 2^24 on the maximum's rounding shows in a fused sum (product())
+    // the exponent of a term is score * factor + base; from 2^24 on the maximum's rounding shows in a fused sum:
+    // product()
     float fac = scale, base = T::kTerm - ms;
     if (!LW && __any(fabsf(ms) >= 16777216.f)) {
 #pragma unroll

@@ -258,8 +258,8 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_ca
     if k_weight is not None:
         kw_at = _floats(k_weight, "k_weight", dev, (dim,))
     _check(_on(dev, lib().kmeans_kv_append)(
-        cache, _DT[dt], T, _ptr(q), hq, qs[0], qs[1], k.data_ptr(), ks[0], ks[1], _ptr(v), vs[0], vs[1], qw_at, kw_at, eps,
-        pos_at, rope_at, max_pos, rot, bool(interleaved), slots_at, _ptr(out) if hq else None, os_[0], os_[1],
+        cache, _DT[dt], T, _ptr(q), hq, qs[0], qs[1], k.data_ptr(), ks[0], ks[1], _ptr(v), vs[0], vs[1], qw_at, kw_at,
+        eps, pos_at, rope_at, max_pos, rot, bool(interleaved), slots_at, _ptr(out) if hq else None, os_[0], os_[1],
         _stream(dev)))
     return out
 

@@ -155,7 +155,8 @@ def _sink(keys, n, hkv, R, at, weighted):
     tol = (2.1 * U[FP] + 4 * es + (keys / 32 + 64) * E)[..., None] * (pr @ vv.abs()) + (
         keys * 2.0 ** -39 * float(vv.abs().max()) + 2.0 ** -25)
     lse = torch.logsumexp(sc, 2)
-    return d, (pr @ vv).transpose(0, 1), tol.transpose(0, 1), lse.t(), (es + (keys / 32 + 64) * E + 4 * E * lse.abs()).t()
+    ltol = es + (keys / 32 + 64) * E + 4 * E * lse.abs()
+    return d, (pr @ vv).transpose(0, 1), tol.transpose(0, 1), lse.t(), ltol.t()
 
 
 @pytest.mark.parametrize("weighted", [False, True])

@@ -180,7 +180,7 @@ def test_buffer_replaced_on_another_stream_is_not_reused_at_once():
 
 
 def test_workspace_that_grows_inside_a_capture():
-    """A larger call captured with a workspace of an eager, smaller one, then eager calls of both sizes between replays."""
+    """A larger call captured with a workspace of an eager, smaller one; eager calls of both sizes between replays."""
     small, large = _inputs(SHAPES[0]), _inputs(SHAPES[2], seed=3)
     ws = kvcache.Workspace(DEV)
     s = torch.cuda.Stream()

@@ -51,7 +51,7 @@ def test_scale_that_overflows_in_units_of_log_2():
     L = kvcache.lib()
     assert _attend(L, scale=3e38) == 1 and "scale" in _said(L)
     assert _attend(L, scale=-3e38) == 1
-    assert _attend(L, scale=3e38, lw=FAKE, ws=None, nb=0) == 3  # (with weights they are natural: only the workspace lacks)
+    assert _attend(L, scale=3e38, lw=FAKE, ws=None, nb=0) == 3  # (natural with weights; the workspace lacks)
 
 
 def test_tensors_that_require_gradients_are_refused():
@@ -94,11 +94,11 @@ def test_attend_of_more_query_heads_than_the_join_takes():
 def test_tables_in_place_are_refused():
     """Lengths that are updated while other workgroups still read them would be a race."""
     L = kvcache.lib()
-    free = dict(ctx=FAKE, new=FAKE + 256, off=FAKE + 512, free=FAKE + 768, seq=FAKE + 1024, qs=FAKE + 1280, ps=FAKE + 1536,
-                pos=FAKE + 1792, slots=FAKE + 2048)
+    names = ("ctx", "new", "off", "free", "seq", "qs", "ps", "pos", "slots")
+    apart = {name: FAKE + 256 * i for i, name in enumerate(names)}
     for out in ("seq", "qs", "ps", "pos", "slots"):
         for given in ("ctx", "new", "off", "free"):
-            assert _tables(L, **dict(free, **{out: free[given]})) == 1 and "must not be an input" in _said(L)
+            assert _tables(L, **dict(apart, **{out: apart[given]})) == 1 and "must not be an input" in _said(L)
 
 
 def test_launches_go_to_the_device_of_the_tensors(monkeypatch):
