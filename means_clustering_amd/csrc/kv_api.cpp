@@ -147,10 +147,12 @@ extern "C" km_status kmeans_kv_tables(const int32_t* ctx_lens, const int32_t* ne
                         (const void*)slots})
     if (!aligned(p, 4)) return invalid("pointers must be 4-byte aligned");
   // the workgroups read the lengths for themselves, at different times
-  for (const void* out : {(const void*)seq_lens, (const void*)query_start, (const void*)page_start,
-                          (const void*)positions, (const void*)slots})
+  // (arrays of no elements may have any address)
+  const void *token_out[2] = {T > 0 ? positions : nullptr, T > 0 ? slots : nullptr};
+  for (const void* out : {(const void*)seq_lens, (const void*)query_start, (const void*)page_start, token_out[0],
+                          token_out[1]})
     for (const void* in : {(const void*)ctx_lens, (const void*)new_lens, (const void*)pos_offset,
-                           (const void*)free_pages})
+                           (const void*)(num_free > 0 ? free_pages : nullptr)})
       if (R > 0 && out && out == in) return invalid("an output must not be an input");
   TablesArgs a;
   a.ctx = ctx_lens;

@@ -40,6 +40,18 @@ def test_tables_pages_that_no_cache_can_have(p):
         assert bool((cache[2, :4] == 1).all()) and float(cache.float().sum()) == 4 * 16
 
 
+def test_tables_arrays_without_elements_have_any_address():
+    """No new tokens and no free pages: their arrays may begin where another one does."""
+    L = kvcache.lib()
+    ctx, new, table = _i32([20, 3]), _i32([0, 0]), _i32([[4, 5], [6, -1]])
+    out = _i32([-9] * 8)
+    at = out.data_ptr()
+    status = L.kmeans_kv_tables(ctx.data_ptr(), new.data_ptr(), None, 2, 16, table.data_ptr(), 2, 2, at, 0, 0, at, at + 8,
+                                at + 20, ctx.data_ptr(), new.data_ptr(), kvcache._stream(0))
+    assert status == 0, L.kmeans_kv_last_error().decode()
+    assert out.tolist() == [20, 3, 0, 0, 0, 0, 0, 0] and ctx.tolist() == [20, 3]
+
+
 # ------------------------------------------------------------------------------------------------------ attend ----
 
 def _check(c, **changes):
