@@ -392,9 +392,11 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 //          is, which is less than 6 * 2^-24 of its value beyond 0.625; for a
 //          negative y without the detour by its sign, two instructions of seven:
 //          by at most 8 * 2^-24.
-// Where no product of the wavefront is beyond 0.625 all are small.  Where one
-// is, all are large if that is off by at most 64 * 8 * 2^-24 = 2^-15 in a score,
-// as much as the products' own rounding; otherwise each takes its own.
+// All are large where that is off by at most 64 * 8 * 2^-24 = 2^-15 in a score, as
+// much as the products' own rounding; for larger caps each takes its own, and
+// where no product of the wavefront is beyond 0.625 only the small way is made.
+// So a score depends on its own product alone: what other rows and keys of the
+// wavefront hold, which its row may not see, leaves every bit of it as it is.
 constexpr float kTanhSmall = 0.625f, kCapExact = 64.f;
 template <int N>
 __device__ __forceinline__ void cap_scores(float* x, float scale, float cap) {
@@ -413,7 +415,7 @@ __device__ __forceinline__ void cap_scores(float* x, float scale, float cap) {
   float far = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) far = fmaxf(far, fabsf(x[i]));
-  if (!__any(far * fabsf(scale) > kTanhSmall)) {
+  if (cap > kCapExact && !__any(far * fabsf(scale) > kTanhSmall)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = small(x[i]);
   } else if (cap <= kCapExact) {

@@ -1,0 +1,92 @@
+"""What a row of the attention's further forms does not see never reaches it, to the last bit; scores at the ends of
+fp32.  References and bounds as in test_gpu_kvcache_forms.py."""
+import math
+
+import pytest
+import torch
+
+from means_clustering_amd import kvcache
+
+from .test_gpu_kvcache import BF, FP
+from .test_gpu_kvcache_forms import FormCase
+
+pytestmark = pytest.mark.gpu
+
+
+def _bits(got):
+    out, lse = got
+    return out.view(torch.int16).cpu(), lse.view(torch.int32).cpu()
+
+
+def _attend(c):
+    return _bits(kvcache.attend(**c.device(), lse=True))
+
+
+def _same(a, b):
+    return torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def _free_page_0(c):
+    """Gives page 0, which stands for pages that are not held where a load needs one, to nobody."""
+    held = set(int(x) for x in c.table.flatten() if x >= 0)
+    if 0 not in held:
+        return
+    other = next(i for i in range(c.k.shape[0]) if i not in held)
+    c.table[c.table == 0] = other
+    arrays = [c.k, c.v] + ([] if c.lw is None else [c.lw]) + ([t for p in c.codes for t in p] if c.eight else [])
+    for t in arrays:
+        t[[0, other]] = t[[other, 0]]
+
+
+def _fill_unseen(c, key, code):
+    """Keys (and codes) of everything that no query sees: slots behind the sequences, pages of nobody, slots that their
+    weight removes, slots in front of the windows."""
+    p, held = c.p, torch.zeros(c.k.shape[:2], dtype=torch.bool)
+    for r, (s, n) in enumerate(c.lens):
+        lo = max(0, s - n - c.window + 1) if c.window else 0
+        for j in range(s):
+            seen = j >= lo or (c.prefix is not None and j < c.prefix[r])
+            page = int(c.table[r, j // p])
+            if seen and 0 <= page < c.k.shape[0] and (c.lw is None or float(c.lw[page, 0, j % p]) > -math.inf):
+                held[page, j % p] = True
+    c.k[~held] = key
+    c.v[~held] = 1.0
+    if c.eight:
+        for codes, _ in c.codes:
+            codes[~held] = code
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("n,hq", [(1, 8), (5, 4), (90, 4)])
+@pytest.mark.parametrize("eight,cap,sharp", [(False, 2.0, 0.3), (False, 30.0, 1.0), (False, 44.0, 0.2),
+                                             (False, 200.0, 1.0), (True, 1.0, 0.2)])
+@pytest.mark.parametrize("window,prefix,weighted", [(0, None, False), (40, [20, 3], False), (50, None, True)])
+def test_capped_rows_do_not_depend_on_what_they_do_not_see(dt, n, hq, eight, cap, sharp, window, prefix, weighted):
+    make = lambda: FormCase([(150, n), (100, n)], hq, 2, 64, dt, window=window, eight=eight, prefix=prefix, cap=cap,
+                            sharp=sharp, weighted=weighted)
+    got = []
+    for key, code in ((0.01, 0), (1e4, 0x7e)):
+        c = make()
+        if weighted:  # (one weight for all heads of a slot)
+            c.lw[:] = c.lw[:, :1]
+        _free_page_0(c)
+        c.table[0, 2] = -1
+        _fill_unseen(c, key, code)
+        got.append(_attend(c))
+    assert _same(*got)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("n", [1, 4, 90])
+@pytest.mark.parametrize("cap", [1.0, 20.0, 100.0])
+def test_capped_rows_do_not_depend_on_other_rows(n, cap, eight):
+    """One head's and one token's queries a thousand times as large: the others' results stay as they are."""
+    c = FormCase([(150, n), (100, n)], 8, 2, 64, BF, cap=cap, sharp=0.1, eight=eight)
+    small = _attend(c)
+    c.q[:, 2] *= 1000
+    c.q[n // 2] *= 1000
+    large = _attend(c)
+    keep = torch.ones(2 * n, 8, dtype=torch.bool)
+    keep[:, 2] = keep[n // 2] = False
+    assert torch.equal(small[0][keep], large[0][keep]) and torch.equal(small[1][keep], large[1][keep])
+    assert not torch.equal(small[0][:, 2], large[0][:, 2])
