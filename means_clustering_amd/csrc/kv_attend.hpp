@@ -392,14 +392,17 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 //          is, which is less than 6 * 2^-24 of its value beyond 0.625; for a
 //          negative y without the detour by its sign, two instructions of seven:
 //          by at most 8 * 2^-24.
-// All are large where that is off by at most 64 * 8 * 2^-24 = 2^-15 in a score, as
-// much as the products' own rounding; for larger caps each takes its own, and
-// where no product of the wavefront is beyond 0.625 only the small way is made.
+// All are large where that is off by at most 64 * 8 * 2^-24 = 2^-15 in a natural
+// score, as much as the products' own rounding: caps up to 64, whatever the unit
+// of the scores is.  For larger caps each takes its own, and where no product of
+// the wavefront is beyond 0.625 only the small way is made.
 // So a score depends on its own product alone: what other rows and keys of the
 // wavefront hold, which its row may not see, leaves every bit of it as it is.
+// NAT: scores are natural, else in units of log 2 (factor(), above).
 constexpr float kTanhSmall = 0.625f, kCapExact = 64.f;
-template <int N>
+template <int N, bool NAT>
 __device__ __forceinline__ void cap_scores(float* x, float scale, float cap) {
+  constexpr float kExact = NAT ? kCapExact : kCapExact * kLog2e;
   auto small = [&](float v) __attribute__((always_inline)) {
     const float y = v * scale, z = y * y;
     float p = fmaf(z, -0.005704986397176981f, 0.02063908614218235f);
@@ -415,10 +418,10 @@ __device__ __forceinline__ void cap_scores(float* x, float scale, float cap) {
   float far = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) far = fmaxf(far, fabsf(x[i]));
-  if (cap > kCapExact && !__any(far * fabsf(scale) > kTanhSmall)) {
+  if (cap > kExact && !__any(far * fabsf(scale) > kTanhSmall)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = small(x[i]);
-  } else if (cap <= kCapExact) {
+  } else if (cap <= kExact) {
     const float both = scale * (2.f * kLog2e);
 #pragma unroll
     for (int i = 0; i < N; ++i)

@@ -370,7 +370,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(A 
         for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int i = 0; i < 16; ++i) x[16 * t + i] = s[t][i];
-        cap_scores<16 * NT>(x, scale, a.cap);
+        cap_scores<16 * NT, LW>(x, scale, a.cap);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll

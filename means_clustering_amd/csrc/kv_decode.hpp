@@ -390,7 +390,7 @@ __global__ __launch_bounds__(kWgThreads, decode_per_cu(DP, 16 * NQ)) void decode
         }
         if constexpr (A::kForm) {
           if (a.cap > 0.f) {
-            cap_scores<8>(s, a.scale, a.cap);
+            cap_scores<8, LW>(s, a.scale, a.cap);
           } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[j] = product(s[j], a.scale);

@@ -90,3 +90,41 @@ def test_capped_rows_do_not_depend_on_other_rows(n, cap, eight):
     keep[:, 2] = keep[n // 2] = False
     assert torch.equal(small[0][keep], large[0][keep]) and torch.equal(small[1][keep], large[1][keep])
     assert not torch.equal(small[0][:, 2], large[0][:, 2])
+
+
+def _one_key_scores(cap, x, chunk, weighted=False, scale=1.0, slopes=None):
+    """lse (and results) of rows that see one key each, whose products are x: with one key lse is the score."""
+    n = len(x)
+    c = FormCase([(n, n)] if chunk else [(1, 1)] * n, 2, 1, 64, BF, window=1, cap=cap, weighted=weighted)
+    c.q[:], c.scale = 0, scale
+    c.q[:, :, 0] = 1.0
+    for i in range(n):
+        key = torch.zeros(64)
+        key[0] = x[i]
+        c.set(0 if chunk else i, i if chunk else 0, k=key.to(BF), lw=0.0 if weighted else None)
+    d = c.device()
+    if slopes is not None:
+        d["slopes"] = slopes
+    out, lse = kvcache.attend(**d, lse=True)
+    v = torch.stack([c.v[int(c.table[0, i // c.p]), i % c.p, 0] if chunk else c.v[int(c.table[i, 0]), 0, 0]
+                     for i in range(n)])
+    assert torch.equal(out.cpu(), v[:, None].expand(n, 2, 64))
+    return lse.double().cpu()
+
+
+@pytest.mark.parametrize("chunk", [False, True])
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("cap", [1.0, 30.0, 44.0, 50.0, 64.0, 64.5, 90.0, 95.0, 1000.0])
+def test_capped_score_of_one_key(cap, weighted, chunk):
+    """With t = tanh y and e = 2^-24: the formula of caps up to 64 is off by 4 e cap, below zero by 5 e |t| cap more; of
+    y itself three roundings (scale / cap, its factor, the product) are 3 e |y| (1 - t^2) <= 1.4 e cap.  Beyond 64 both
+    are parts of the score: 6 e of it and, |y| (1 - t^2) <= |t|, 3 e.  Then the cap in its unit, log 2 and the products
+    with them: 4 e of the score."""
+    y = torch.tensor([0.001, 0.01, 0.1, 0.3, 0.5, 0.62, 0.63, 0.7, 1.0, 1.5, 2.0, 3.0, 5.0, 9.0, 30.0])
+    x = (torch.cat([y, -y, torch.zeros(1)]) * cap).to(BF)
+    lse = _one_key_scores(cap, x, chunk, weighted)
+    t = torch.tanh(x.double() / cap)
+    e, s = 2.0 ** -24, (cap * t).abs()
+    tol = (5.4 + 5 * (t < 0) * t.abs()) * e * cap + 4 * e * s if cap <= 64 else 13 * e * s
+    off = (lse - (cap * t)[:, None]).abs() - tol[:, None]
+    assert float(off.max()) <= 0, off
