@@ -413,7 +413,8 @@ __device__ __forceinline__ void cap_scores(float* x, float scale, float cap) {
   };
   const float twice = fabsf(scale) * (2.f * kLog2e), sign = scale < 0.f ? -1.f : 1.f;
   auto large = [&](float v) __attribute__((always_inline)) {
-    return __builtin_copysignf(fmaf(-2.f * cap, __builtin_amdgcn_rcpf(exp2_(fabsf(v) * twice) + 1.f), cap), v * sign);
+    const float t = fmaf(-2.f, __builtin_amdgcn_rcpf(exp2_(fabsf(v) * twice) + 1.f), 1.f);
+    return __builtin_copysignf(product(cap, t), v * sign);  // (2 cap can overflow)
   };
   float far = 0.f;
 #pragma unroll

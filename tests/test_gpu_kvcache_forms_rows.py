@@ -128,3 +128,15 @@ def test_capped_score_of_one_key(cap, weighted, chunk):
     tol = (5.4 + 5 * (t < 0) * t.abs()) * e * cap + 4 * e * s if cap <= 64 else 13 * e * s
     off = (lse - (cap * t)[:, None]).abs() - tol[:, None]
     assert float(off.max()) <= 0, off
+
+
+@pytest.mark.parametrize("chunk", [False, True])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_caps_near_the_end_of_fp32(weighted, chunk):
+    """Twice the cap is no float; the score is, as near as beyond a cap of 64."""
+    cap, scale = 2e38, 4.0
+    y = torch.tensor([0.1, 0.6, 0.7, 1.0, 2.0, 5.0])
+    k = (torch.cat([y, -y, torch.zeros(1)]) * (cap / scale)).to(BF)
+    lse = _one_key_scores(cap, k, chunk, weighted, scale=scale)
+    s = cap * torch.tanh(k.double() * (scale / cap))
+    assert bool(((lse - s[:, None]).abs() <= 13 * 2.0 ** -24 * s.abs()[:, None]).all()), lse
