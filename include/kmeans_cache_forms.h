@@ -109,7 +109,8 @@ km_status kmeans_kv_read(const km_kv_cache* cache, const km_kv_scales* scales, k
  * is a part of the prompt whose tokens see one another, or with a window the
  * slots (sinks, centroids) that stay in sight.
  * Limits: cap 0 (none) or positive and finite, scale and cap finite times
- * log2(e) without weights, scale / cap finite and 0 or at least 2^-126.
+ * log2(e) without weights, scale / cap finite times 2 log2(e) and 0 or at least
+ * 2^-126.
  */
 typedef struct km_kv_scores {
   float scale;

@@ -239,8 +239,9 @@ extern "C" km_status kmeans_kv_attend_form(const km_kv_cache* cache, const km_kv
   const float cap = scores->cap * log2e, unit = scores->cap > 0.f ? scores->scale / scores->cap : scores->scale * log2e;
   if (!(scores->cap >= 0.f) || !std::isfinite(cap))
     return invalid("cap must be 0 (none) or positive and finite, times log2(e) too");
-  if (!std::isfinite(scores->scale) || !std::isfinite(unit))
-    return invalid("scale must be finite, times log2(e) and over cap too");
+  // (over the cap it is the factor of a tanh's argument, which is taken times 2 log2(e))
+  if (!std::isfinite(scores->scale) || !std::isfinite(scores->cap > 0.f ? unit * (2.f * 1.4426950408889634f) : unit))
+    return invalid("scale must be finite, times log2(e) and over cap (times 2 log2(e)) too");
   if (scores->cap > 0.f && scores->scale != 0.f && !(std::fabs(unit) >= 1.17549435e-38f))
     return invalid("scale / cap must not be below 2^-126");
   if (width < 0 || width > kMaxRoom / cache->page_size || table_stride < width || table_stride >= kMaxStride)
