@@ -102,7 +102,8 @@ km_status kmeans_kv_read(const km_kv_cache* cache, const km_kv_scales* scales, k
  * The scores of an attention.  A query at slot p and a key at slot j, with
  * x = scale * (q . k_j):
  *   s = cap * tanh(x / cap) (cap > 0; else x) + log_weight_j - slope_h * |p - j|
- * (a distance in fp32: beyond 2^24 slots rounded to 24 bits).
+ * (a distance in fp32: beyond 2^24 slots rounded to 24 bits; a score that
+ * overflows to -inf counts as one that is not seen).
  * slopes: device fp32[q_heads] or NULL.  The query sees slot j of its request
  * (below seq_lens[r]) if j < prefix[r] (device int32[R] or NULL; wherever the
  * query stands), or if j <= p and, with window > 0, j > p - window.  So a prefix

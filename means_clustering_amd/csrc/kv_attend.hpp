@@ -369,6 +369,13 @@ template <bool NAT>
 __device__ __forceinline__ float factor(float s, float m) {
   return exp2_(NAT ? (s - m) * kLog2e : s - m);
 }
+// A slope in the scores' unit.  A finite one stays finite: at distance 0 it takes
+// nothing from a score.
+template <bool NAT>
+__device__ __forceinline__ float slope_of(float s) {
+  const float v = NAT ? s : s * kLog2e;
+  return fabsf(v) == INFINITY && fabsf(s) != INFINITY ? __builtin_copysignf(3.402823466e38f, s) : v;
+}
 // The softmax term of a score, times 2^kTerm.
 template <class T, bool NAT>
 __device__ __forceinline__ float term(float s, float m) {

@@ -166,7 +166,7 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(A 
   const int see1 = min(c + wq1 + 1, end), see0 = a.window > 0 ? c + wq0 - a.window + 1 : 0;
   const int wfull1 = min(c + tok0 + 1, end), wfull0 = a.window > 0 ? c + tok1 - a.window + 1 : 0;
   float slope = 0.f;
-  if constexpr (EX) slope = a.slopes ? a.slopes[hq] * (LW ? 1.f : kLog2e) : 0.f;
+  if constexpr (EX) slope = a.slopes ? slope_of<LW>(a.slopes[hq]) : 0.f;
   // (a tile of slots kt .. that all of the workgroup's rows see)
   auto all_see = [&](int kt) __attribute__((always_inline)) {
     if constexpr (EX)

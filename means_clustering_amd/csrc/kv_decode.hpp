@@ -289,7 +289,7 @@ __global__ __launch_bounds__(kWgThreads, decode_per_cu(DP, 16 * NQ)) void decode
         }
       }
       if constexpr (A::kForm) {
-        slope[q] = a.slopes ? a.slopes[hq] * (LW ? 1.f : kLog2e) : 0.f;
+        slope[q] = a.slopes ? slope_of<LW>(a.slopes[hq]) : 0.f;
         c_of[q] = c + i;
       }
       jmax[q] = min(c + i, end - 1);

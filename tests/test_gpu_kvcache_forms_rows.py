@@ -7,7 +7,7 @@ import torch
 
 from means_clustering_amd import kvcache
 
-from .test_gpu_kvcache import BF, FP
+from .test_gpu_kvcache import BF, DEV, FP
 from .test_gpu_kvcache_forms import FormCase
 
 pytestmark = pytest.mark.gpu
@@ -140,3 +140,20 @@ def test_caps_near_the_end_of_fp32(weighted, chunk):
     lse = _one_key_scores(cap, k, chunk, weighted, scale=scale)
     s = cap * torch.tanh(k.double() * (scale / cap))
     assert bool(((lse - s[:, None]).abs() <= 13 * 2.0 ** -24 * s.abs()[:, None]).all()), lse
+
+
+@pytest.mark.parametrize("chunk", [False, True])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_slopes_near_the_end_of_fp32(weighted, chunk):
+    """At distance 0 a finite slope takes nothing, even where times log2(e) it is no float; beyond, nothing is left."""
+    slopes = torch.tensor([3e38, 2.5e38], device=DEV)
+    x = torch.tensor([0.0, 1.0, -3.0, 0.5])
+    lse = _one_key_scores(0.0, x, chunk, weighted, slopes=slopes)
+    assert float((lse - x.double()[:, None]).abs().max()) <= 8 * 2.0 ** -24 * 3
+    n = 70 if chunk else 1
+    c = FormCase([(100, n)], 2, 1, 64, BF, weighted=weighted)
+    if weighted:
+        c.lw.zero_()
+    out = kvcache.attend(**dict(c.device(), slopes=slopes)).cpu()
+    own = torch.stack([c.v[int(c.table[0, j // 16]), j % 16, 0] for j in range(100 - n, 100)])
+    assert torch.equal(out, own[:, None].expand(n, 2, 64))
