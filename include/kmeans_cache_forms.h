@@ -77,8 +77,9 @@ typedef struct km_kv_turn {
  * (the tables of kmeans_kv_tables put them side by side); no two share a slot.
  * Without v values and their scales are not touched (scales->v may be NULL).
  * Limits as kmeans_kv_append.  With an 8-bit cache T * heads <= 2^26 - 4, k and v
- * are different arrays, and pages, slots and heads must not overlap (strides of
- * at least dim where there are several).
+ * are different arrays, and pages, slots and heads must not overlap: in the order
+ * of their strides, each of which there are several steps over all of the smaller
+ * ones.
  */
 km_status kmeans_kv_append_form(const km_kv_cache* cache, const km_kv_scales* scales, km_dtype dt, int64_t T,
                                 const void* q, int64_t q_heads, int64_t q_token, int64_t q_head, const void* k,

@@ -38,9 +38,20 @@ const char* codes_error(const km_kv_cache* c, const km_kv_scales* s, bool need_k
   return nullptr;
 }
 
-// Whether pages, slots and heads of codes lie apart.
+// Whether pages, slots and heads of codes lie apart: in the order of their strides each steps over all of the smaller
+// ones.  (What the move of older codes reads nobody else writes then.)
 bool apart(const km_kv_cache* c, int64_t page, int64_t slot, int64_t head) {
-  return (c->pages == 1 || page >= c->dim) && slot >= c->dim && (c->heads == 1 || head >= c->dim);
+  struct {
+    int64_t step, n;
+  } d[3] = {{page, c->pages}, {slot, c->page_size}, {head, c->heads}};
+  std::sort(d, d + 3, [](const auto& x, const auto& y) { return x.step < y.step; });
+  int64_t span = c->dim;  // (no stride reaches kMaxStride)
+  for (const auto& i : d) {
+    if (i.n == 1) continue;
+    if (i.step < span) return false;
+    span = i.n - 1 > (kMaxStride - span) / i.step ? kMaxStride : span + (i.n - 1) * i.step;
+  }
+  return true;
 }
 
 km_status dtype_error(km_dtype dt) {
