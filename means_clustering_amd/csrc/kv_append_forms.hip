@@ -22,8 +22,11 @@
 // in registers; rows of blocks that reach over the window's ends are made beside
 // it, for their A only.  The rows' maxima meet in LDS, each group takes those of
 // its block's tokens (at most 15 places away), and writes its row; the group of
-// the block's first token writes the scale.  Queries (and with a 16-bit cache all
-// rows) are rows on their own, as in kv_append.hip.
+// the block's first token writes the scale.  Two workgroups may so work out the
+// scale of one block, each for its own tokens, and have to agree: what makes a row
+// is fused by hand or not at all (norm(), turn()), so its copies round alike.
+// Queries (and with a 16-bit cache all rows) are rows on their own, as in
+// kv_append.hip.
 //
 // Measured (bf16, 8 cache heads of 128): 16,001 tokens 46 us for keys and values
 // (98 MB, 22 us at a copy's rate) and 57 us for 32 heads of queries (HBM); what
@@ -101,6 +104,7 @@ __device__ __forceinline__ V join_lanes(V v, Op op) {
 
 template <int LPR, bool PAIRS>
 __device__ __forceinline__ void norm(const FormAppendArgs& a, const Lane<PAIRS>& l, const float* weight, float* x) {
+#pragma clang fp contract(off)
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
@@ -168,8 +172,8 @@ __device__ __forceinline__ void turn(const Angles& v, float* x) {
   for (int i = 0; i < 8; ++i) {
     const int ia = PAIRS ? 2 * i : i, ib = PAIRS ? 2 * i + 1 : 8 + i;
     const float p = x[ia], r = x[ib];
-    x[ia] = p * v.c[i] - r * v.s[i];
-    x[ib] = r * v.c[i] + p * v.s[i];
+    x[ia] = fmaf(p, v.c[i], -(r * v.s[i]));
+    x[ib] = fmaf(r, v.c[i], p * v.s[i]);
   }
 }
 
