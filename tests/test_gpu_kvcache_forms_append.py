@@ -9,7 +9,7 @@ import torch
 from means_clustering_amd import kvcache
 
 from .test_gpu_kvcache import BF, DEV, FP, _rope
-from .test_gpu_kvcache_forms import F8, _check_block_rows, _random_cache, _turned
+from .test_gpu_kvcache_forms import F8, _check_append8, _check_block_rows, _random_cache, _turned
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,32 @@ def test_queries_are_the_same_in_every_call(dt, pairs, norm):
     whole = whole.to(DEV)  # slots of blocks that one of the small calls writes as a whole
     assert torch.equal(codes.view(-1, D)[:T][whole], kc.view(torch.uint8).view(-1, D)[:T][whole])
     assert torch.equal(scale.view(-1).repeat_interleave(16)[:T][whole], ks.view(-1).repeat_interleave(16)[:T][whole])
+
+
+def _ragged(T, short=40):
+    """A long run in the middle of a block, short ones (decode steps and a few tokens) and a second long one."""
+    runs = [(i % 16, 1 + i % 3) for i in range(short)]
+    left = T - sum(n for _, n in runs)
+    return [(5, left * 2 // 3)] + runs + [(11, left - left * 2 // 3)]
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("T,hq,hkv,D,rot,pairs,norm,layout,axes,values", [
+    (5500, 13, 3, 256, 256, False, True, "packed", None, True),   # odd heads, the last workgroup has one; queries apart
+    (5500, 1, 3, 256, 128, True, True, "plain", 3, False),        # keys alone
+    (6700, 0, 5, 128, 128, False, True, "packed", None, True),
+    (8300, 4, 4, 128, 96, True, False, "heads", 2, True),
+    (2100, 32, 8, 256, 256, False, False, "packed", 3, True),
+    (9400, 1, 7, 48, 32, False, True, "packed", 4, False)])
+def test_large_appends(dt, T, hq, hkv, D, rot, pairs, norm, layout, axes, values):
+    """Workgroups of two heads: where windows of 4,096 / lanes tokens times heads reach 1,024; from 65,536 rows of D =
+    256 (131,072 of 128) on the queries have a launch of their own."""
+    lanes = next(n for n in (2, 4, 8, 16) if 16 * n >= D)
+    assert -(-T * lanes // 256) * hkv >= 1024
+    _check_append8(_ragged(T), hq, hkv, D, 16, dt, rot, pairs, norm, layout, axes, padding=True, seed=T, values=values)
+
+
+def test_large_appends_of_few_heads():
+    """One head a workgroup, and windows of which the last has few tokens."""
+    _check_append8(_ragged(8209), 9, 1, 128, 64, BF, seed=1)
+    _check_append8(_ragged(4097), 17, 2, 256, 32, FP, rot=64, axes=3, mix=0, seed=2)
