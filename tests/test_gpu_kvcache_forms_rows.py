@@ -157,3 +157,40 @@ def test_slopes_near_the_end_of_fp32(weighted, chunk):
     out = kvcache.attend(**dict(c.device(), slopes=slopes)).cpu()
     own = torch.stack([c.v[int(c.table[0, j // 16]), j % 16, 0] for j in range(100 - n, 100)])
     assert torch.equal(out, own[:, None].expand(n, 2, 64))
+
+
+@pytest.mark.parametrize("what", ["key", "value", "key scale", "value scale"])
+@pytest.mark.parametrize("dt,n,hq,D", [(BF, 1, 8, 64), (FP, 4, 4, 128), (BF, 90, 4, 64), (FP, 70, 2, 80), (BF, 1, 4, 256),
+                                       (BF, 60, 2, 256)])
+@pytest.mark.parametrize("window,prefix,weighted,cap", [(0, None, False, 0.0), (40, None, True, 0.0),
+                                                        (40, [30, 60], False, 5.0)])
+def test_unseen_nan_codes_and_scales_do_not_reach_a_row(what, dt, n, hq, D, window, prefix, weighted, cap):
+    """NaN codes of a slot, or a scale of 255 for a block's 16 slots: rows that see one of them are NaN, all others have
+    the bits that they have without."""
+    bad = {0: [149, 100, 2], 1: [99, 50, 20]}  # slots; of a scale their blocks
+    make = lambda: FormCase([(150, n), (100, n)], hq, 2, D, dt, window=window, eight=True, prefix=prefix,
+                            weighted=weighted, cap=cap)
+    clean = make()
+    want = kvcache.attend(**clean.device()).cpu()
+    for r, js in bad.items():
+        for j in js:
+            c = make()
+            page = int(c.table[r, j // 16])
+            codes, scale = c.codes["value" in what]
+            if "scale" in what:
+                scale[page] = 255
+                hit = range(j - j % 16, min(j - j % 16 + 16, c.lens[r][0]))
+            else:
+                codes[page, j % 16] = 0xff
+                hit = [j]
+            got = kvcache.attend(**c.device()).cpu()
+            for t in range(2 * n):
+                mine, i = (t // n == r), t % n
+                pos = c.lens[r][0] - n + i
+                sees = torch.zeros(2, dtype=torch.bool)
+                for s in hit if mine else ():
+                    if (s <= pos and (not window or s > pos - window)) or (prefix and s < prefix[r]):
+                        sees |= torch.ones(2, dtype=torch.bool) if c.lw is None else c.lw[page, :, s % 16] > -math.inf
+                sees = sees.repeat_interleave(hq // 2)
+                assert bool(got[t][sees].isnan().all()), (r, j, t)
+                assert torch.equal(got[t][~sees].view(torch.int16), want[t][~sees].view(torch.int16)), (r, j, t)
