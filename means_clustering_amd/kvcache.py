@@ -474,6 +474,8 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
         dt = k_cache.dtype
     dev, dim = k_cache.get_device(), cache.dim
     form = scales is not None or softcap != 0 or slopes is not None or prefix_lens is not None
+    if softcap != 0 and ctypes.c_float(softcap).value == 0:
+        raise ValueError(f"softcap must be 0 (none) or no less than fp32's least number, got {softcap}")
     shape = q.shape
     T, hq = (shape[0], shape[1]) if len(shape) == 3 else (0, 0)  # (of another number of dimensions _rows refuses it)
     qs = _rows(q, "q", dev, dt, (T, hq, dim))

@@ -194,3 +194,13 @@ def test_unseen_nan_codes_and_scales_do_not_reach_a_row(what, dt, n, hq, D, wind
                 sees = sees.repeat_interleave(hq // 2)
                 assert bool(got[t][sees].isnan().all()), (r, j, t)
                 assert torch.equal(got[t][~sees].view(torch.int16), want[t][~sees].view(torch.int16)), (r, j, t)
+
+
+@pytest.mark.parametrize("cap", [1e-50, -1e-50, 1e-46])
+def test_caps_that_fp32_has_not(cap):
+    """Rounded to 0 it would mean no cap at all."""
+    d = FormCase([(20, 1)], 2, 1, 64, BF).device()
+    with pytest.raises(ValueError, match="softcap"):
+        kvcache.attend(**dict(d, softcap=cap))
+    kvcache.attend(**dict(d, softcap=0.0))
+    kvcache.attend(**dict(d, softcap=0))
