@@ -455,7 +455,16 @@ __global__ __launch_bounds__(kThreads, F8 ? 4 : 8) void append_form_kernel(FormA
   write_row<T, LPR, PAIRS, F8>(a, group * kRows + threadIdx.x / LPR);
 }
 
-constexpr int64_t kApart = 4096;  // workgroups of queries
+// Queries of more workgroups than this have a launch of their own.  Measured, the append alone (bf16), with the writers
+// / apart: 32 + 8 heads of 128 2,047 workgroups 15.9 / 20.3 us, 4,095 26.7 / 32.6, 8,191 54.3 / 57.7, 16,001 101.8 /
+// 97.1; 28 + 4 heads by 3 axes 3,583 22.3 / 25.9, 5,250 36.4 / 37.9, 7,167 48.4 / 44.9, 14,000 92.2 / 76.9; 16 + 8 heads
+// of 256 8,191 77.1 / 81.9.  (So the two meet between 5,500 and 12,000 or later by shape, and from here to there apart
+// costs up to 20%.)
+constexpr int64_t kApart = 4096;
+// Workgroups for each compute unit from which two heads share one.  Measured, one head / two, by windows times heads: 8
+// heads of 128 512 11.7 / 12.6 us, 752 16.0 / 14.1, 1,024 19.0 / 16.3, 4,008 71.4 / 55.8; 4 heads by 3 axes 376 12.4 /
+// 12.9, 512 14.4 / 13.9, 1,024 22.5 / 20.6; 8 heads of 256 504 14.5 / 15.1, 1,024 22.5 / 19.9; 16 heads of 64 512 11.6 /
+// 12.7, 752 15.4 / 13.9.  (They meet between 450 and 700.)
 constexpr int64_t kPerCu = 4;
 
 template <class T, int LPR>

@@ -393,8 +393,9 @@ __device__ __forceinline__ float log_sum(float m, float l) {
 
 // Scores s = cap * tanh(x * scale) of N products x of a lane.  Two ways to a
 // tanh:
-//   small  y + y^3 P(y^2), P a fit of least relative error to (tanh y / y - 1) /
-//          y^2 for |y| <= 0.625: off by at most 1.4 * 2^-24 of its value;
+//   small  y + y^3 P(y^2), fitted to tanh for |y| <= 0.625 so that their largest
+//          relative difference is least (0.15 * 2^-24): off by at most 1.4 * 2^-24
+//          of its value with its roundings;
 //   large  1 - 2 / (e^2|y| + 1) with y's sign: off by at most 4 * 2^-24 whatever y
 //          is, which is less than 6 * 2^-24 of its value beyond 0.625; for a
 //          negative y without the detour by its sign, two instructions of seven:
