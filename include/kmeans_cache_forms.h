@@ -75,6 +75,8 @@ typedef struct km_kv_turn {
  * (Scale bytes of 0 and 255 count as 1 and 254 here.)
  * The tokens of a block must stand within 15 places of one another in the call
  * (the tables of kmeans_kv_tables put them side by side); no two share a slot.
+ * Nothing looks for others: the block that they share, no more, then holds
+ * anything.
  * Without v values and their scales are not touched (scales->v may be NULL).
  * Limits as kmeans_kv_append.  With an 8-bit cache T * heads <= 2^26 - 4, k and v
  * are different arrays, and pages, slots and heads must not overlap: in the order
@@ -105,6 +107,7 @@ km_status kmeans_kv_read(const km_kv_cache* cache, const km_kv_scales* scales, k
  *   s = cap * tanh(x / cap) (cap > 0; else x) + log_weight_j - slope_h * |p - j|
  * (a distance in fp32: beyond 2^24 slots rounded to 24 bits; a score that
  * overflows to -inf counts as one that is not seen).
+ * Distances and windows count slots, whatever a slot stands for.
  * slopes: device fp32[q_heads] or NULL.  The query sees slot j of its request
  * (below seq_lens[r]) if j < prefix[r] (device int32[R] or NULL; wherever the
  * query stands), or if j <= p and, with window > 0, j > p - window.  So a prefix

@@ -47,8 +47,9 @@
 //   * fp16: terms times 2^14, 0.6% slower than without.
 //
 // Forms (4,096 tokens over 12,288 slots before them, 32 + 8 heads of 128, where
-// the plain kernel takes 1,098-1,117 us): a prefix 1,090-1,116, slopes
-// 1,253-1,292, a cap 1,371-1,514 (vector units 60% busy with it, matrix cores 29%).
+// the plain kernel takes 1,098-1,117 us): a prefix 1,090-1,125, slopes
+// 1,253-1,292, a cap of up to 64 1,220-1,333 (vector units 60% busy with it, matrix
+// cores 29%), a larger one, with scores beyond 0.625 of it, 1,665-1,767.
 // An 8-bit cache 1,133-1,180, half the bytes for a conversion more; its tiles
 // pass through registers, fetched a tile ahead and put into LDS as 16-bit values
 // behind the products, so that the products are the same.

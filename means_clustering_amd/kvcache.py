@@ -339,7 +339,8 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor | None, k_ca
     ``axes`` (uint8 [rot / 2]) with ``positions`` int32 [1 to 4, T] turns pair i by the position on axis axes[i] (time,
     height, width; kmeans_kv_append_form).  ``k_scale`` and ``v_scale`` make the cache an 8-bit one: new rows share a
     scale with the block of 16 slots that they fall into, which grows as they need, and a call that writes a block's
-    first slot begins the block anew.  The tokens of a block stand within 15 places of one another.
+    first slot begins the block anew, whatever its other slots held.  The tokens of a block stand within 15 places of one
+    another (nothing looks for others: their block would hold anything).
     """
     if _recording():
         for t in (q, k, v, k_cache, v_cache, q_weight, k_weight, rope, out):
@@ -456,8 +457,9 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
 
     Further forms (kmeans_kv_attend_form): ``k_scale`` and ``v_scale`` make the cache an 8-bit one (q and out stay 16
     bits); ``softcap`` c > 0 makes a score x into c * tanh(x / c), before its weight; ``slopes`` (fp32 [q_heads])
-    subtracts slope * |distance| of the slots; all queries of request r see its slots below ``prefix_lens[r]`` (int32
-    [R]), wherever they stand and whatever the window is.
+    subtracts slope * |distance| of the slots (as ``window``, not of the positions: a centroid is as far away as its
+    slot, whatever tokens it stands for); all queries of request r see its slots below ``prefix_lens[r]`` (int32 [R]),
+    wherever they stand and whatever the window is.
     """
     if _recording() and (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad or (
             out is not None and out.requires_grad) or (log_weight is not None and log_weight.requires_grad) or (
