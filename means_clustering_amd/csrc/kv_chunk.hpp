@@ -444,13 +444,14 @@ __global__ __launch_bounds__(kWgThreads, DP == 256 ? 1 : 2) void chunk_kernel(A 
     // the exponent of a term is score * factor + base; from 2^24 on the maximum's rounding shows in a fused sum:
     // product()
     float fac = EX ? 1.f : scale, base = T::kTerm - ms;
-    if (!LW && !EX && __any(fabsf(ms) >= 16777216.f)) {
+    const bool far = !LW && !EX && fabsf(ms) >= 16777216.f;
+    if (__any(far)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[t][i] = product(s[t][i], scale) - ms;
-      fac = 1.f;
-      base = T::kTerm;
+        for (int i = 0; i < 16; ++i) s[t][i] = far ? product(s[t][i], scale) - ms : s[t][i];
+      fac = far ? 1.f : fac;
+      base = far ? T::kTerm : base;
     }
     float sum = 0.f;
     auto values = [&](int u, u32x4_t(&vf)[DT]) __attribute__((always_inline)) {
