@@ -115,8 +115,8 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a) {
       const float c = i < 4 ? ca[i & 3] : cb[i & 3], s = i < 4 ? sa[i & 3] : sb[i & 3];
       const int ia = PAIRS ? 2 * i : i, ib = PAIRS ? 2 * i + 1 : 8 + i;
       const float p = x[ia], r = x[ib];
-      x[ia] = p * c - r * s;
-      x[ib] = r * c + p * s;
+      x[ia] = fmaf(p, c, -(r * s));  // (fused by hand, as in kv_append_forms.hip: a row has the same bits from both)
+      x[ib] = fmaf(r, c, p * s);
     }
   }
   if (mine) {
